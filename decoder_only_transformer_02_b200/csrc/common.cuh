@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -16,6 +17,10 @@ enum DeviceErr : int {
   DERR_TOKEN_RANGE = 1,     // a token or target id >= padded vocab
   DERR_WAIT_TIMEOUT = 2,    // an mbarrier wait ran past its limit
   DERR_NONFINITE = 3,       // non-finite gradient norm (update skipped)
+  // refused by a paged-cache kernel (GPT2_ECACHE; codes from DERR_KV8_ARGS on)
+  DERR_KV8_ARGS = 16,   // a slot, length or row offset out of range, or a slot named twice
+  DERR_KV8_PAGES = 17,  // not enough free pages
+  DERR_KV8_TABLE = 18,  // a page table entry outside the pool, or of a free page
 };
 
 // (the library is one translation unit, so this is its single definition)

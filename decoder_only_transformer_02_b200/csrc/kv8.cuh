@@ -1,0 +1,678 @@
+// Paged key/value cache held in 8 bits: the layout, the page table's
+// operations (resize, fork, compact) and the append that rounds new keys and
+// values into it.  The attention that reads it is in kv8_attention.cuh.
+//
+// A page holds page_size tokens of every layer:
+//   codes  [num_pages][n_layer][2][n_kv_head][page_size][head_dim]  8 bits (side 0 keys, 1 values)
+//   scales [num_pages][n_layer][2][n_kv_head]                       fp32, powers of two
+// so a page is one contiguous block (copied by fork and compact as such) and
+// the tokens of one (page, layer, side, head) are one contiguous tile, which
+// the attention streams.  A value is code * scale.
+//   table  [num_slots][max_pages]  page ids of a slot's tokens, in order
+//   lens   [num_slots]             cached tokens of a slot
+//   refs   [num_pages]             slots that hold the page (0: free)
+//
+// Why powers of two: x / scale is then exact, so a code is one rounding of the
+// value itself, and the codes do not depend on how the division was computed;
+// when a page's scale grows, e4m3 codes move by whole exponents (exact down to
+// their subnormals).  The price is up to one bit of the int8 range (scale up
+// to 2 * amax / 127).  The smallest scale is 2^-126.
+#pragma once
+#include "../../include/gpt2.h"
+#include "common.cuh"
+
+namespace kv8 {
+
+constexpr int MAX_SEQS = 4096;      // entries of one call (their offsets are scanned in shared memory)
+constexpr int MAX_SLOTS = 1 << 16;  // the duplicate check's bitmap is 8 KB of shared memory
+constexpr int MAX_PAGES = 1 << 24;
+constexpr int MAX_TOKENS = 1 << 30;  // of a slot
+constexpr uint32_t NAN_SCALE = 0x7fc00000u;
+
+struct Cache {
+  int fmt, L, kvh, d, ps, ps_log2, num_pages, num_slots, max_pages;
+  uint8_t* codes;
+  float* scales;
+  int32_t *table, *lens, *refs;
+  __host__ __device__ long tile() const { return (long)ps * d; }                     // bytes of one head's tokens
+  __host__ __device__ long page_bytes() const { return 2L * L * kvh * ps * d; }
+  __host__ __device__ int page_scales() const { return 2 * L * kvh; }
+  // index of (page, layer, side, head) among the tiles and scales
+  __device__ __forceinline__ long unit(int page, int layer, int side, int head) const {
+    return (((long)page * L + layer) * 2 + side) * kvh + head;
+  }
+  __device__ __forceinline__ bool page_ok(int p) const { return (unsigned)p < (unsigned)num_pages; }
+  __device__ __forceinline__ int pages_of(int len) const { return (int)(((long)len + ps - 1) >> ps_log2); }
+  // length of a slot; -1 (flagged) when the slot or its length is out of range
+  __device__ __forceinline__ int len_of(int slot) const {
+    if ((unsigned)slot >= (unsigned)num_slots) return -1;
+    const int len = lens[slot];
+    return len < 0 || pages_of(len) > max_pages ? -1 : len;
+  }
+};
+
+// griddepcontrol: the second kernel of a pair is launched while the first
+// runs and waits here for its results
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ------------------------------------------------------------------- append
+// Rounding of the new tokens of one (page, layer, side, head), by one warp:
+//   amax over the new values; scale' = 2^e, the smallest (e >= -126) with
+//   amax <= qmax 2^e, or the page's old scale if that is larger and the page
+//   already holds older tokens; codes round(x / scale') to nearest even.
+// A scale that grows rescales the whole tile's codes first.  A value that is
+// not finite makes the scale NaN: the block then reads as NaN.
+__device__ __forceinline__ uint32_t scale_bits_for(uint32_t amax_bf16, int fmt) {
+  const int E = (int)(amax_bf16 >> 7), m = (int)(amax_bf16 & 127);
+  if (E == 255) return NAN_SCALE;
+  // 127 = (1 + 126/128) 2^6, 448 = (1 + 96/128) 2^8; the exponent field of scale'
+  const int e = fmt == GPT2_KV_INT8 ? E - (m <= 126 ? 6 : 5) : E - (m <= 96 ? 8 : 7);
+  return (uint32_t)max(e, 1) << 23;
+}
+// 1 / scale of a power of two from 2^-126 to 2^126 (exponent fields 1..253)
+__device__ __forceinline__ float inverse_pow2(uint32_t bits) { return __uint_as_float(0x7f000000u - bits); }
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  if (FMT == GPT2_KV_E4M3) return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+  const int x = __float2int_rn(a), y = __float2int_rn(b), z = __float2int_rn(c), w = __float2int_rn(d);
+  return (uint32_t)(x & 255) | ((uint32_t)(y & 255) << 8) | ((uint32_t)(z & 255) << 16) | ((uint32_t)w << 24);
+}
+template <int FMT>
+__device__ __forceinline__ void unpack4(uint32_t w, float (&f)[4]) {
+  if (FMT == GPT2_KV_E4M3) {
+    const uint32_t lo = e4m3x2_to_half2(w & 0xffffu), hi = e4m3x2_to_half2(w >> 16);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+  }
+}
+
+constexpr int APPEND_WARPS = 8;
+
+// CTA (x, y): x names a run of one sequence's new tokens inside one page, y a
+// group of APPEND_WARPS of the 2 * kvh (side, head) pairs, one warp each.
+// by_row: x is a row, and works if its token is the run's first.  Otherwise x
+// counts runs: sequence i owns the numbers from cu[i] / ps + 2 i, enough since
+// its q tokens touch at most q / ps + 2 pages; no prefix sum is needed.
+template <int FMT>
+__global__ void __launch_bounds__(32 * APPEND_WARPS)
+    append_kernel(Cache c, int layer, const bf16* __restrict__ k, const bf16* __restrict__ v, long ld,
+                  const int32_t* __restrict__ slots, const int32_t* __restrict__ cu, int n, int rows, int by_row) {
+  __shared__ int s_i, s_a, s_b, s_slot;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int x = blockIdx.x;
+  if (tid == 0) s_i = -1;
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += blockDim.x) {
+    const int a = cu[i], b = cu[i + 1];
+    const bool mine = by_row ? x >= a && x < b
+                             : x >= (a >> c.ps_log2) + 2 * i && x < (b >> c.ps_log2) + 2 * i + 2;
+    bad |= a < 0 || b < a || b > rows;
+    if (mine) s_i = i, s_a = a, s_b = b, s_slot = slots[i];  // one thread at most, unless the offsets are bad
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) set_device_err(DERR_KV8_ARGS);
+    return;
+  }
+  const int i = s_i;
+  if (i < 0) return;
+  const int a = s_a, q = s_b - a, slot = s_slot;
+  // a slot named twice: the later entries are refused, or both would write the same tokens
+  bool twice = false;
+  for (int j = tid; j < i; j += blockDim.x) twice |= slots[j] == slot && cu[j + 1] > cu[j];
+  twice = __syncthreads_or(twice);
+  if (q == 0) return;
+  const int len = c.len_of(slot);
+  if (len < q || twice) {
+    if (tid == 0) set_device_err(DERR_KV8_ARGS);
+    return;
+  }
+  const int p0 = len - q;  // position of the sequence's first new token
+  int pos, end;
+  if (by_row) {
+    pos = p0 + (x - a);
+    if (x != a && (pos & (c.ps - 1)) != 0) return;
+  } else {
+    const int j = x - ((a >> c.ps_log2) + 2 * i);
+    pos = j == 0 ? p0 : ((p0 >> c.ps_log2) + j) << c.ps_log2;
+    if (pos >= len) return;
+  }
+  end = min(len, (pos | (c.ps - 1)) + 1);
+  const int pair = blockIdx.y * APPEND_WARPS + warp;
+  if (pair >= 2 * c.kvh) return;
+  const int side = pair >= c.kvh, head = pair - side * c.kvh;
+  const int page = c.table[(long)slot * c.max_pages + (pos >> c.ps_log2)];
+  if (!c.page_ok(page)) {
+    if (lane == 0) set_device_err(DERR_KV8_TABLE);
+    return;
+  }
+  const long u = c.unit(page, layer, side, head);
+  const int d8 = c.d >> 3, m = end - pos;       // 16-byte pieces of a row; rows
+  const int per = 32 / d8, sub = lane / d8;     // rows a warp reads at once; this lane's
+  const bf16* src = (side ? v : k) + (long)(a + pos - p0) * ld + head * c.d + (lane % d8) * 8;
+  // pass 1: the largest magnitude, as bf16 bits (their order is the values')
+  uint32_t mx = 0;
+  for (int r = sub; r < m; r += per) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + (long)r * ld);
+    const uint32_t t0 = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+    const uint32_t t1 = __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+    mx = __vmaxu2(mx, __vmaxu2(t0, t1));
+  }
+  mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+  const int off = pos & (c.ps - 1);
+  uint32_t bits = scale_bits_for(mx, FMT);
+  uint8_t* tile = c.codes + u * c.tile();
+  if (off != 0) {
+    const uint32_t old = __float_as_uint(c.scales[u]);
+    if (bits > old && bits != NAN_SCALE) {  // positive floats and the NaN order as their bits
+      const float ratio = __uint_as_float(old) * inverse_pow2(bits);
+      for (int t = lane; t < (int)(c.tile() >> 4); t += 32) {
+        uint4 w = reinterpret_cast<uint4*>(tile)[t];
+        uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float f[4];
+          unpack4<FMT>(e[g], f);
+          e[g] = pack4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+        }
+        reinterpret_cast<uint4*>(tile)[t] = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+    }
+    bits = max(bits, old);
+  }
+  __syncwarp();  // every lane has read the old scale, and the rescaled codes come before the new ones
+  if (lane == 0) c.scales[u] = __uint_as_float(bits);
+  const float inv = bits >= NAN_SCALE ? 0.f : inverse_pow2(bits);
+  const bool nan = bits >= NAN_SCALE;
+  // pass 2: the codes
+  uint8_t* dst = tile + (long)off * c.d + (lane % d8) * 8;
+  for (int r = sub; r < m; r += per) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + (long)r * ld);
+    const float2 f0 = unpack_bf16x2(w.x), f1 = unpack_bf16x2(w.y), f2 = unpack_bf16x2(w.z), f3 = unpack_bf16x2(w.w);
+    uint2 o;
+    o.x = pack4<FMT>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
+    o.y = pack4<FMT>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
+    if (nan) o = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(dst + (long)r * c.d) = o;
+  }
+}
+
+static inline cudaError_t append(const Cache& c, int layer, const bf16* k, const bf16* v, long ld,
+                                 const int32_t* slots, const int32_t* cu, int n, int rows, cudaStream_t st) {
+  if (n == 0 || rows == 0) return cudaSuccess;
+  const long runs = (long)(rows >> c.ps_log2) + 2L * n;
+  const int by_row = rows <= runs;
+  const dim3 grid((unsigned)(by_row ? rows : runs), (2 * c.kvh + APPEND_WARPS - 1) / APPEND_WARPS);
+  if (c.fmt == GPT2_KV_INT8)
+    append_kernel<GPT2_KV_INT8><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row);
+  else
+    append_kernel<GPT2_KV_E4M3><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------- page table: plan and apply
+// resize, fork and compact run as two kernels.  The plan (one CTA) checks the
+// arguments, so that a refused call changes nothing, and finds the pages: free
+// pages are handed out lowest first, in the order of the list.  The apply
+// kernel (many CTAs) rewrites the tables and counts and copies the pages.
+// The workspace (32-bit words):
+//   head[16]: 0 go, 1 copies, 2 pages wanted, 3 live pages, 4 live pages below the live count
+//   first[n]: the number of pages wanted by the entries before
+//   copy[2 n]: source page and destination's number among the free pages of each copy
+//   list[3 num_pages]: free pages in order; (compact) holes, high pages by live rank, live rank of a page
+constexpr int HEAD = 16;
+constexpr int PLAN_THREADS = 1024;
+
+struct Work {
+  int32_t *head, *first, *copy, *list, *high, *rank;
+};
+static inline Work work_of(void* w, int n, int num_pages) {
+  int32_t* p = static_cast<int32_t*>(w);
+  Work k;
+  k.head = p;
+  k.first = p + HEAD;
+  k.copy = k.first + n;
+  k.list = k.copy + 2L * n;
+  k.high = k.list + num_pages;
+  k.rank = k.high + num_pages;
+  return k;
+}
+static inline size_t workspace_bytes(int n, int num_pages) { return 4 * (HEAD + 3 * (size_t)n + 3 * (size_t)num_pages); }
+
+// exclusive prefix sum over the block; `total` receives the sum
+__device__ __forceinline__ int block_scan(int v, int& total, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // s_warp is free again
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  total = s_warp[31];
+  return x - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// The wanted lowest free pages (refs 0) into list; returns how many there are
+// (at least `want`, or all of them).
+__device__ __forceinline__ int find_free(const Cache& c, int want, int32_t* list, int* s_warp) {
+  int found = 0;
+  for (int base = 0; base < c.num_pages && found < want; base += 4 * PLAN_THREADS) {
+    const int p = base + 4 * threadIdx.x;
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p + 3 < c.num_pages) {
+      r = __ldcg(reinterpret_cast<const int4*>(c.refs + p));
+    } else {
+      if (p < c.num_pages) r.x = __ldcg(c.refs + p);
+      if (p + 1 < c.num_pages) r.y = __ldcg(c.refs + p + 1);
+      if (p + 2 < c.num_pages) r.z = __ldcg(c.refs + p + 2);
+    }
+    int total;
+    int at = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), total, s_warp);
+    if (r.x == 0 && at < want) list[at] = p;
+    at += r.x == 0;
+    if (r.y == 0 && at < want) list[at] = p + 1;
+    at += r.y == 0;
+    if (r.z == 0 && at < want) list[at] = p + 2;
+    at += r.z == 0;
+    if (r.w == 0 && at < want) list[at] = p + 3;
+    found += total;
+  }
+  return found;
+}
+
+// What a resize does to one slot.
+struct Change {
+  int have, want, edge, copy, src;  // pages before and after; the page kept in part: its column, whether copied, its id
+};
+__device__ __forceinline__ Change change_of(const Cache& c, int slot, int old_len, int new_len) {
+  Change h;
+  h.have = c.pages_of(old_len);
+  h.want = c.pages_of(new_len);
+  const int keep = min(old_len, new_len);
+  h.edge = keep >> c.ps_log2;
+  h.copy = 0;
+  h.src = -1;
+  if (keep & (c.ps - 1)) {
+    h.src = c.table[(long)slot * c.max_pages + h.edge];
+    if (!c.page_ok(h.src))
+      h.copy = -1;
+    else
+      h.copy = c.refs[h.src] > 1;
+  }
+  return h;
+}
+
+// Every slot in range and none named twice (a bitmap in shared memory).
+__device__ __forceinline__ bool claim(const Cache& c, int slot, uint32_t* s_map) {
+  if ((unsigned)slot >= (unsigned)c.num_slots) return false;
+  return !(atomicOr(&s_map[slot >> 5], 1u << (slot & 31)) >> (slot & 31) & 1u);
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS)
+    resize_plan_kernel(Cache c, const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int n, Work w) {
+  extern __shared__ uint32_t s_map[];
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch();
+  for (int i = tid; i < (c.num_slots + 31) / 32; i += PLAN_THREADS) s_map[i] = 0;
+  __syncthreads();
+  int err = 0, want = 0, copies = 0;
+  for (int base = 0; base < n; base += PLAN_THREADS) {
+    const int i = base + tid;
+    int need = 0, copy = 0, src = 0;
+    if (i < n) {
+      const int slot = slots[i], new_len = lens[i];
+      const int old_len = c.len_of(slot);
+      if (!claim(c, slot, s_map) || old_len < 0 || new_len < 0 || c.pages_of(new_len) > c.max_pages) {
+        err = DERR_KV8_ARGS;
+      } else {
+        const Change h = change_of(c, slot, old_len, new_len);
+        if (h.copy < 0) err = DERR_KV8_TABLE;
+        copy = h.copy > 0, src = h.src;
+        need = copy + max(0, h.want - h.have);
+      }
+    }
+    int total;
+    const int at = want + block_scan(need, total, s_warp);
+    if (i < n) w.first[i] = at;
+    want += total;
+    const int k = copies + block_scan(copy, total, s_warp);
+    if (copy) {
+      w.copy[2 * k] = src;
+      w.copy[2 * k + 1] = at;
+    }
+    copies += total;
+  }
+  // pages given back: every id is checked before the first count changes
+  int bad = 0;
+  if (__syncthreads_or(err) == 0) {
+    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
+      const int slot = slots[i], have = c.pages_of(c.lens[slot]);
+      for (int j = c.pages_of(lens[i]) + lane; j < have; j += 32)
+        if (!c.page_ok(c.table[(long)slot * c.max_pages + j])) bad = 1;
+    }
+    if (bad) err = DERR_KV8_TABLE;
+  }
+  if (__syncthreads_or(err) != 0) {
+    if (err) set_device_err(err);
+    if (tid == 0) w.head[0] = 0;
+    return;
+  }
+  for (int sign = -1; sign <= 1; sign += 2) {  // give back; a second time, with +1, only where too few are free
+    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
+      const int slot = slots[i], have = c.pages_of(c.lens[slot]);
+      for (int j = c.pages_of(lens[i]) + lane; j < have; j += 32)
+        atomicAdd(&c.refs[c.table[(long)slot * c.max_pages + j]], sign);
+    }
+    __syncthreads();
+    if (sign > 0) {
+      if (tid == 0) {
+        set_device_err(DERR_KV8_PAGES);
+        w.head[0] = 0;
+      }
+      return;
+    }
+    if (find_free(c, want, w.list, s_warp) >= want) break;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    w.head[0] = 1;
+    w.head[1] = copies;
+    w.head[2] = want;
+  }
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS)
+    fork_plan_kernel(Cache c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, Work w) {
+  extern __shared__ uint32_t s_map[];
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch();
+  for (int i = tid; i < (c.num_slots + 31) / 32; i += PLAN_THREADS) s_map[i] = 0;
+  __syncthreads();
+  int err = 0, want = 0;
+  for (int base = 0; base < n; base += PLAN_THREADS) {
+    const int i = base + tid;
+    int part = 0, page = 0;
+    if (i < n) {
+      const int len = c.len_of(src[i]);
+      if (len < 0 || !claim(c, dst[i], s_map) || c.lens[dst[i]] != 0) {
+        err = DERR_KV8_ARGS;
+      } else if (len & (c.ps - 1)) {
+        part = 1;
+        page = c.table[(long)src[i] * c.max_pages + (len >> c.ps_log2)];
+      }
+    }
+    int total;
+    const int at = want + block_scan(part, total, s_warp);
+    if (i < n) w.first[i] = at;
+    if (part) {
+      w.copy[2 * at] = page;
+      w.copy[2 * at + 1] = at;
+    }
+    want += total;
+  }
+  int bad = 0;
+  if (__syncthreads_or(err) == 0) {
+    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
+      const int used = c.pages_of(c.lens[src[i]]);
+      for (int j = lane; j < used; j += 32)
+        if (!c.page_ok(c.table[(long)src[i] * c.max_pages + j])) bad = 1;
+    }
+    if (bad) err = DERR_KV8_TABLE;
+  }
+  if (__syncthreads_or(err) == 0 && find_free(c, want, w.list, s_warp) < want && tid == 0) err = DERR_KV8_PAGES;
+  if (__syncthreads_or(err) != 0) {
+    if (err) set_device_err(err);
+    if (tid == 0) w.head[0] = 0;
+    return;
+  }
+  if (tid == 0) {
+    w.head[0] = 1;
+    w.head[1] = want;
+    w.head[2] = want;
+  }
+}
+
+// n_live = pages with refs > 0.  The j-th live page with an id of n_live or
+// more moves to the j-th free page below n_live.  high[live rank] and rank[id]
+// are written for the pages that move, list[j] for the holes.
+__global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Work w) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch();
+  int err = 0;
+  for (int i = warp; i < c.num_slots; i += PLAN_THREADS / 32) {
+    const int len = c.len_of(i);
+    if (len < 0) err = DERR_KV8_ARGS;
+    const int used = len < 0 ? 0 : c.pages_of(len);
+    for (int j = lane; j < used; j += 32) {
+      const int page = c.table[(long)i * c.max_pages + j];
+      if (!c.page_ok(page) || c.refs[page] <= 0) err = DERR_KV8_TABLE;
+    }
+  }
+  if (__syncthreads_or(err) != 0) {
+    if (err) set_device_err(err);
+    if (tid == 0) w.head[0] = 0;
+    return;
+  }
+  int live = 0;
+  for (int p = tid; p < c.num_pages; p += PLAN_THREADS) live += c.refs[p] > 0;
+  block_scan(live, live, s_warp);
+  if (tid == 0 && live == c.num_pages) w.head[4] = live;
+  int before = 0;
+  for (int base = 0; base < c.num_pages; base += PLAN_THREADS) {
+    const int p = base + tid;
+    const int is = p < c.num_pages && c.refs[p] > 0;
+    int total;
+    const int r = before + block_scan(is, total, s_warp);  // live pages below p
+    if (p < c.num_pages) {
+      if (p == live) w.head[4] = r;
+      if (p < live && !is) w.list[p - r] = p;
+      if (p >= live && is) {
+        w.high[r] = p;
+        w.rank[p] = r;
+      }
+    }
+    before += total;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    w.head[0] = 1;
+    w.head[3] = live;
+    w.head[1] = live - w.head[4];
+  }
+}
+
+// Copies of whole pages (codes and scales), a grid-stride loop over pieces of
+// 16 KB: four 16-byte loads in flight per thread.
+constexpr int COPY_THREADS = 256;
+constexpr int COPY_PIECE = COPY_THREADS * 64;
+template <class Pair>
+__device__ __forceinline__ void copy_pages(const Cache& c, int copies, Pair pair) {
+  const long bytes = c.page_bytes();
+  const int pieces = (int)((bytes + COPY_PIECE - 1) / COPY_PIECE);
+  const long all = (long)copies * pieces;
+  for (long t = blockIdx.x; t < all; t += gridDim.x) {
+    const int k = (int)(t / pieces), piece = (int)(t % pieces);
+    int src, dst;
+    pair(k, src, dst);
+    const long at = (long)piece * COPY_PIECE;
+    const uint4* s = reinterpret_cast<const uint4*>(c.codes + src * bytes + at);
+    uint4* o = reinterpret_cast<uint4*>(c.codes + dst * bytes + at);
+    const int m = (int)((min(bytes - at, (long)COPY_PIECE)) >> 4);
+    uint4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((int)threadIdx.x + e * COPY_THREADS < m) x[e] = __ldcs(s + threadIdx.x + e * COPY_THREADS);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((int)threadIdx.x + e * COPY_THREADS < m) __stcs(o + threadIdx.x + e * COPY_THREADS, x[e]);
+    if (piece == 0) {
+      const int ns = c.page_scales();
+      for (int e = threadIdx.x; e < ns; e += COPY_THREADS) c.scales[(long)dst * ns + e] = c.scales[(long)src * ns + e];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(COPY_THREADS)
+    resize_apply_kernel(Cache c, const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int n, Work w) {
+  pdl_wait();
+  if (w.head[0] == 0) return;
+  const int lane = threadIdx.x & 31;
+  // A slot's copied page shows in the lists: its destination is the first of the pages it wanted.
+  for (int i = blockIdx.x * (COPY_THREADS / 32) + (threadIdx.x >> 5); i < n; i += gridDim.x * (COPY_THREADS / 32)) {
+    const int slot = slots[i], new_len = lens[i], old_len = c.lens[slot];
+    const int first = w.first[i], next = i + 1 < n ? w.first[i + 1] : w.head[2];
+    const int have = c.pages_of(old_len), want = c.pages_of(new_len);
+    const int copy = next - first - max(0, want - have);
+    int32_t* row = c.table + (long)slot * c.max_pages;
+    __syncwarp();
+    if (lane == 0) {
+      if (copy) {
+        const int edge = min(old_len, new_len) >> c.ps_log2, page = w.list[first];
+        atomicAdd(&c.refs[row[edge]], -1);
+        row[edge] = page;
+        c.refs[page] = 1;
+      }
+      c.lens[slot] = new_len;
+    }
+    for (int j = have + lane; j < want; j += 32) {
+      const int page = w.list[first + copy + j - have];
+      row[j] = page;
+      c.refs[page] = 1;
+    }
+    for (int j = want + lane; j < have; j += 32) row[j] = -1;
+  }
+  copy_pages(c, w.head[1], [&](int k, int& src, int& dst) {
+    src = w.copy[2 * k];
+    dst = w.list[w.copy[2 * k + 1]];
+  });
+}
+
+__global__ void __launch_bounds__(COPY_THREADS)
+    fork_apply_kernel(Cache c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, Work w) {
+  pdl_wait();
+  if (w.head[0] == 0) return;
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * (COPY_THREADS / 32) + (threadIdx.x >> 5); i < n; i += gridDim.x * (COPY_THREADS / 32)) {
+    const int len = c.lens[src[i]], whole = len >> c.ps_log2;
+    const int32_t* from = c.table + (long)src[i] * c.max_pages;
+    int32_t* to = c.table + (long)dst[i] * c.max_pages;
+    for (int j = lane; j < whole; j += 32) {
+      const int page = from[j];
+      to[j] = page;
+      atomicAdd(&c.refs[page], 1);
+    }
+    if (lane == 0 && (len & (c.ps - 1))) {
+      const int page = w.list[w.first[i]];
+      to[whole] = page;
+      c.refs[page] = 1;
+    }
+    if (lane == 0) c.lens[dst[i]] = len;
+  }
+  copy_pages(c, w.head[1], [&](int k, int& s, int& t) {
+    s = w.copy[2 * k];
+    t = w.list[w.copy[2 * k + 1]];
+  });
+}
+
+__global__ void __launch_bounds__(COPY_THREADS) compact_apply_kernel(Cache c, int32_t* live_out, Work w) {
+  pdl_wait();
+  if (w.head[0] == 0) return;
+  const int lane = threadIdx.x & 31, low = w.head[4], live = w.head[3], moves = w.head[1];
+  const int stride = gridDim.x * COPY_THREADS, me = blockIdx.x * COPY_THREADS + threadIdx.x;
+  for (int j = me; j < moves; j += stride) {
+    const int from = w.high[low + j], to = w.list[j];
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+  }
+  for (int i = me >> 5; i < c.num_slots; i += stride >> 5) {
+    int32_t* row = c.table + (long)i * c.max_pages;
+    const int used = c.pages_of(c.lens[i]);
+    for (int j = lane; j < used; j += 32)
+      if (row[j] >= live) row[j] = w.list[w.rank[row[j]] - low];
+  }
+  if (me == 0 && live_out) *live_out = live;
+  copy_pages(c, moves, [&](int k, int& s, int& t) {
+    s = w.high[low + k];
+    t = w.list[k];
+  });
+}
+
+// The apply kernel starts while the plan runs (programmatic dependent launch)
+// and waits for it in pdl_wait().
+template <class... P, class... A>
+static inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                       A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+constexpr int APPLY_CTAS = 148 * 6;
+
+static inline cudaError_t resize(const Cache& c, const int32_t* slots, const int32_t* lens, int n, void* work,
+                                 cudaStream_t st) {
+  if (n == 0) return cudaSuccess;
+  const Work w = work_of(work, n, c.num_pages);
+  resize_plan_kernel<<<1, PLAN_THREADS, (size_t)((c.num_slots + 31) / 32) * 4, st>>>(c, slots, lens, n, w);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(resize_apply_kernel, dim3(APPLY_CTAS), COPY_THREADS, 0, st, c, slots, lens, n, w);
+}
+static inline cudaError_t fork(const Cache& c, const int32_t* src, const int32_t* dst, int n, void* work,
+                               cudaStream_t st) {
+  if (n == 0) return cudaSuccess;
+  const Work w = work_of(work, n, c.num_pages);
+  fork_plan_kernel<<<1, PLAN_THREADS, (size_t)((c.num_slots + 31) / 32) * 4, st>>>(c, src, dst, n, w);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(fork_apply_kernel, dim3(APPLY_CTAS), COPY_THREADS, 0, st, c, src, dst, n, w);
+}
+static inline cudaError_t compact(const Cache& c, int32_t* live, void* work, cudaStream_t st) {
+  const Work w = work_of(work, 0, c.num_pages);
+  compact_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(c, w);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(compact_apply_kernel, dim3(APPLY_CTAS), COPY_THREADS, 0, st, c, live, w);
+}
+
+}  // namespace kv8

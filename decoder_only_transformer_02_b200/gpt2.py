@@ -18,7 +18,8 @@ _lib = None
 
 GPT2_FP32 = 0
 GPT2_BF16 = 1
-_ERRS = {-1: "EINVAL", -2: "ECUDA", -3: "ETOKEN", -4: "ENOMEM", -5: "ESTATE", -6: "ENONFINITE"}
+_ERRS = {-1: "EINVAL", -2: "ECUDA", -3: "ETOKEN", -4: "ENOMEM", -5: "ESTATE", -6: "ENONFINITE",
+         -7: "ECACHE"}
 
 EXPORTED = [
     "gpt2_create", "gpt2_destroy", "gpt2_set_stream", "gpt2_forward", "gpt2_backward", "gpt2_forward_backward",
@@ -29,8 +30,12 @@ EXPORTED = [
     "gpt2_matmul_bf16", "gpt2_matmul_workspace_bytes", "gpt2_set_timing", "gpt2_get_timing",
     "gpt2_attention_backward_noalloc", "gpt2_set_graphs", "gpt2_check_device_error", "gpt2_set_wait_limit_ns",
     "gpt2_prefill", "gpt2_decode_step", "gpt2_get_decode_logits", "gpt2_check_guards",
-    "gpt2_debug_overwrite_guard",
+    "gpt2_debug_overwrite_guard", "gpt2_kv8_workspace_bytes", "gpt2_kv8_resize", "gpt2_kv8_fork",
+    "gpt2_kv8_compact", "gpt2_kv8_append", "gpt2_kv8_attention_workspace_bytes", "gpt2_kv8_attention",
 ]
+GPT2_KV_INT8 = 0
+GPT2_KV_E4M3 = 1
+KV8_MAX_SEQS = 4096
 ATTN_NOALLOC_MAX_ROWS = 1 << 19  # padded (batch, head, position) rows
 KCLASSES = ["matmul", "attention_fwd", "attention_bwd", "layernorm_fwd", "layernorm_bwd", "cross_entropy",
             "optimizer", "embedding", "other"]
@@ -46,6 +51,12 @@ class GPT2Error(RuntimeError):
 class _Config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("n_layer", "n_head", "n_embd", "vocab_size", "padded_vocab",
                                              "block_size", "max_B", "max_T", "precision")]
+
+
+class _KV8(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("format", "n_layer", "n_kv_head", "head_dim", "page_size", "num_pages",
+                                             "num_slots", "max_pages")] +
+                [(n, ctypes.c_void_p) for n in ("d_codes", "d_scales", "d_table", "d_lens", "d_refs")])
 
 
 def library_path() -> str:
@@ -101,6 +112,13 @@ def load_library():
         "gpt2_prefill": (I, [P, P, I, I, F, I, ctypes.c_uint64, P]),
         "gpt2_decode_step": (I, [P, P, I, I, F, I, ctypes.c_uint64, P]),
         "gpt2_get_decode_logits": (I, [P, P]),
+        "gpt2_kv8_workspace_bytes": (S, [P, I]),
+        "gpt2_kv8_resize": (I, [P, P, P, I, P, S, P]),
+        "gpt2_kv8_fork": (I, [P, P, P, I, P, S, P]),
+        "gpt2_kv8_compact": (I, [P, P, P, S, P]),
+        "gpt2_kv8_append": (I, [P, I, P, P, L, P, P, I, I, P]),
+        "gpt2_kv8_attention_workspace_bytes": (S, [P, I, I, I, I]),
+        "gpt2_kv8_attention": (I, [P, I, P, L, P, L, P, I, P, P, I, I, I, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -373,10 +391,151 @@ def matmul_workspace_bytes(M, N, K) -> int:
     return int(load_library().gpt2_matmul_workspace_bytes(M, N, K))
 
 
+class KV8Cache:
+    """Paged key/value cache held in 8 bits (the gpt2_kv8_* calls) in the
+    caller's CUDA tensors, which the handle keeps alive:
+      codes   int8 or float8_e4m3fn [num_pages, n_layer, 2, n_kv_head, page_size, head_dim]
+      scales  float32 [num_pages, n_layer, 2, n_kv_head]
+      table   int32 [num_slots, max_pages];  lens  int32 [num_slots];  refs  int32 [num_pages]
+    An empty cache has lens and refs all zero (KV8Cache.allocate makes one).
+    The calls are asynchronous on `stream` (None: the legacy default stream)
+    and run on the tensors' device; what only the device can refuse is raised
+    by check_device_error() as ECACHE."""
+
+    def __init__(self, codes, scales, table, lens, refs):
+        import torch
+        fmts = {torch.int8: GPT2_KV_INT8, torch.float8_e4m3fn: GPT2_KV_E4M3}
+        self._torch = torch
+        dev = codes.device
+        shapes_ok = codes.dim() == 6 and codes.shape[2] == 2 and codes.dtype in fmts and dev.type == "cuda" and \
+            scales.dtype == torch.float32 and tuple(scales.shape) == tuple(codes.shape[:4]) and \
+            table.dim() == 2 and tuple(lens.shape) == (table.shape[0],) and tuple(refs.shape) == (codes.shape[0],)
+        if not shapes_ok or any(t.dtype != torch.int32 for t in (table, lens, refs)) or \
+                any(t.device != dev or not t.is_contiguous() for t in (codes, scales, table, lens, refs)):
+            raise GPT2Error(-1, "KV8Cache: codes, scales, table, lens, refs have the wrong shape, type, layout or device")
+        self.codes, self.scales, self.table, self.lens, self.refs = codes, scales, table, lens, refs
+        self.num_pages, self.n_layer, _, self.n_kv_head, self.page_size, self.head_dim = codes.shape
+        self.num_slots, self.max_pages = table.shape
+        self.device = dev
+        self._c = _KV8(fmts[codes.dtype], self.n_layer, self.n_kv_head, self.head_dim, self.page_size, self.num_pages,
+                       self.num_slots, self.max_pages, codes.data_ptr(), scales.data_ptr(), table.data_ptr(),
+                       lens.data_ptr(), refs.data_ptr())
+        self._p = ctypes.addressof(self._c)
+        self._lib = load_library()
+        if self._lib.gpt2_kv8_workspace_bytes(self._p, 0) == 0:
+            raise GPT2Error(-1, "KV8Cache: a size outside the library's limits, or codes / refs not 16-byte aligned")
+
+    @classmethod
+    def allocate(cls, fmt, n_layer, n_kv_head, head_dim, page_size, num_pages, num_slots, max_pages, device="cuda"):
+        """An empty cache; fmt GPT2_KV_INT8 or GPT2_KV_E4M3."""
+        import torch
+        dtypes = {GPT2_KV_INT8: torch.int8, GPT2_KV_E4M3: torch.float8_e4m3fn}
+        if fmt not in dtypes:
+            raise GPT2Error(-1, "KV8Cache: unknown format")
+        raw = torch.zeros(num_pages, n_layer, 2, n_kv_head, page_size, head_dim, dtype=torch.int8, device=device)
+        return cls(raw.view(dtypes[fmt]),
+                   torch.ones(num_pages, n_layer, 2, n_kv_head, dtype=torch.float32, device=device),
+                   torch.full((num_slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(num_slots, dtype=torch.int32, device=device),
+                   torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+    def workspace_bytes(self, n) -> int:
+        """Bytes of `work` for resize, fork (up to n entries) and compact."""
+        return int(self._lib.gpt2_kv8_workspace_bytes(self._p, n))
+
+    def attention_workspace_bytes(self, n_head, n, rows, max_q) -> int:
+        return int(self._lib.gpt2_kv8_attention_workspace_bytes(self._p, n_head, n, rows, max_q))
+
+    def _call(self, what, fn, *args):
+        if self._torch.cuda.current_device() == self.device.index:
+            r = fn(*args)
+        else:
+            with self._torch.cuda.device(self.device):
+                r = fn(*args)
+        if r != 0:
+            raise GPT2Error(r, what)
+
+    def _ints(self, what, *tensors):
+        i32, dev = self._torch.int32, self.device
+        for t in tensors:
+            if t.dtype is not i32 or t.device != dev or t.dim() != 1 or not t.is_contiguous():
+                raise GPT2Error(-1, what + ": index arrays are contiguous one-dimensional int32 tensors on the cache's device")
+
+    def _work(self, what, work):
+        if work.device != self.device or not work.is_contiguous():
+            raise GPT2Error(-1, what + ": work is a contiguous tensor on the cache's device")
+        return work.data_ptr(), work.numel() * work.element_size()
+
+    def _rows(self, what, t, heads):
+        """Row stride of a bf16 [rows, heads, head_dim] view whose rows are contiguous."""
+        if t.dtype is not self._torch.bfloat16 or t.device != self.device or t.dim() != 3 or t.shape[1] != heads or \
+                t.shape[2] != self.head_dim or t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
+            raise GPT2Error(-1, what + ": rows are bf16 [rows, heads, head_dim] with contiguous heads on the cache's device")
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * self.head_dim)
+
+    def resize(self, slots, new_lens, work, stream=None):
+        """slots[i] to the length new_lens[i] (device int32); 0 frees the slot."""
+        self._ints("gpt2_kv8_resize", slots, new_lens)
+        if slots.shape != new_lens.shape:
+            raise GPT2Error(-1, "gpt2_kv8_resize: one length for each slot")
+        w, nb = self._work("gpt2_kv8_resize", work)
+        self._call("gpt2_kv8_resize", self._lib.gpt2_kv8_resize, self._p, slots.data_ptr(), new_lens.data_ptr(),
+                   slots.shape[0], w, nb, _stream_ptr(stream))
+
+    def fork(self, src, dst, work, stream=None):
+        """The empty slots dst[i] take over the tokens of src[i] (device int32)."""
+        self._ints("gpt2_kv8_fork", src, dst)
+        if src.shape != dst.shape:
+            raise GPT2Error(-1, "gpt2_kv8_fork: one destination for each source")
+        w, nb = self._work("gpt2_kv8_fork", work)
+        self._call("gpt2_kv8_fork", self._lib.gpt2_kv8_fork, self._p, src.data_ptr(), dst.data_ptr(), src.shape[0], w,
+                   nb, _stream_ptr(stream))
+
+    def compact(self, work, live=None, stream=None):
+        """Pages in use to the lowest ids; live: device int32 [1] that receives their number."""
+        if live is not None:
+            self._ints("gpt2_kv8_compact", live)
+        w, nb = self._work("gpt2_kv8_compact", work)
+        self._call("gpt2_kv8_compact", self._lib.gpt2_kv8_compact, self._p, _ptr(live), w, nb, _stream_ptr(stream))
+
+    def append(self, layer, k, v, slots, cu, stream=None):
+        """k, v: bf16 [rows, n_kv_head, head_dim], of the same row stride (views
+        of a fused projection will do); rows cu[i]..cu[i+1]-1 are the last
+        tokens of slots[i]."""
+        self._ints("gpt2_kv8_append", slots, cu)
+        ld = self._rows("gpt2_kv8_append", k, self.n_kv_head)
+        if v.shape != k.shape or self._rows("gpt2_kv8_append", v, self.n_kv_head) != ld or \
+                cu.shape[0] != slots.shape[0] + 1:
+            raise GPT2Error(-1, "gpt2_kv8_append: k and v have one shape and stride, cu one offset more than slots")
+        self._call("gpt2_kv8_append", self._lib.gpt2_kv8_append, self._p, layer, k.data_ptr(), v.data_ptr(), ld,
+                   slots.data_ptr(), cu.data_ptr(), slots.shape[0], k.shape[0], _stream_ptr(stream))
+
+    def attention(self, layer, q, out, slots, cu, max_q, work, lse=None, stream=None):
+        """Causal attention of q (bf16 [rows, n_head, head_dim], views with a row
+        stride will do) over the cached tokens into out (the same shape); lse:
+        None or float32 [rows, n_head].  No sequence has more than max_q rows."""
+        what = "gpt2_kv8_attention"
+        self._ints(what, slots, cu)
+        rows, heads = q.shape[0], q.shape[1]
+        ldq, ldo = self._rows(what, q, heads), self._rows(what, out, heads)
+        if out.shape[0] != rows or cu.shape[0] != slots.shape[0] + 1:
+            raise GPT2Error(-1, what + ": out has q's shape, cu one offset more than slots")
+        if lse is not None and (lse.dtype is not self._torch.float32 or lse.device != self.device or
+                                tuple(lse.shape) != (rows, heads) or not lse.is_contiguous()):
+            raise GPT2Error(-1, what + ": lse is a contiguous float32 [rows, n_head] on the cache's device")
+        w, nb = self._work(what, work)
+        self._call(what, self._lib.gpt2_kv8_attention, self._p, layer, q.data_ptr(), ldq, out.data_ptr(), ldo,
+                   _ptr(lse), heads, slots.data_ptr(), cu.data_ptr(), slots.shape[0], rows, max_q, w, nb,
+                   _stream_ptr(stream))
+
+
 def check_device_error(stream=None):
     """Synchronise `stream`, then read and clear the device's error word:
-    raises GPT2Error (ECUDA) when a kernel gave up on a wait since the last check."""
-    _op_check(load_library().gpt2_check_device_error(_stream_ptr(stream)), "a device-side wait gave up")
+    raises GPT2Error (ECUDA) when a kernel gave up on a wait since the last
+    check, or (ECACHE) when a paged-cache call was refused on the device."""
+    r = load_library().gpt2_check_device_error(_stream_ptr(stream))
+    _op_check(r, "refused by the paged cache (slot, length, row offset, page or no free page)" if r == -7
+              else "a device-side wait gave up")
 
 
 def set_wait_limit_ns(limit_ns: int):

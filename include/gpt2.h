@@ -47,6 +47,7 @@ extern "C" {
 #define GPT2_ENOMEM (-4)     /* device or host allocation failed */
 #define GPT2_ESTATE (-5)     /* call out of order (e.g. backward without a forward with targets) */
 #define GPT2_ENONFINITE (-6) /* non-finite gradient norm: the AdamW update was skipped */
+#define GPT2_ECACHE (-7)     /* refused on the device by a paged-cache call: bad slot, length, row offset or page, or no free page */
 
 #define GPT2_FP32 0 /* fp32 everywhere, CUDA-core (FFMA) matmuls: the parity mode */
 #define GPT2_BF16 1 /* bf16 tensor-core matmuls and attention, fp32 master weights,
@@ -241,6 +242,100 @@ int gpt2_matmul_bf16(const void* d_A, int64_t lda, int a_mn, const void* d_B, in
 /* Bytes of d_work with which an epi = 5 call of this shape splits over K. */
 size_t gpt2_matmul_workspace_bytes(int M, int N, int K);
 
+/* ---- paged key/value cache held in 8 bits (device pointers, caller-owned memory) ----
+ * (No counterpart in the paper.)  Keys and values of many sequences of
+ * different lengths in pages of page_size tokens that sequences can share.
+ * A page holds every layer; a value is code * scale, with one scale for each
+ * page, layer, side (0 keys, 1 values) and head, always a power of two.
+ * Slot s holds d_lens[s] tokens; token t is in page d_table[s][t / page_size].
+ * An empty cache is d_lens and d_refs all 0; codes, scales and table entries
+ * that no token uses are never read.  The caller owns all memory, and the
+ * calls below are the only writers of lens, table, refs and scales.
+ *
+ * All calls are asynchronous, allocate nothing, can be captured in a CUDA
+ * graph and take effect in stream order; with n or rows 0 they do nothing.  The host checks sizes and pointers
+ * (GPT2_EINVAL, nothing enqueued).  What only the device knows (slots,
+ * lengths, row offsets, page ids, free pages) is checked there: a refused call
+ * or sequence records GPT2_ECACHE, which gpt2_check_device_error (below, or
+ * the next syncing call of a model handle) returns; no kernel traps.  Calls
+ * that overlap in time need a workspace each, and must not name the same
+ * slots unless both only read (attention); resize, fork and compact change
+ * d_refs and must not overlap each other. */
+#define GPT2_KV_INT8 0 /* signed 8-bit integers, -127..127 */
+#define GPT2_KV_E4M3 1 /* 8-bit floats, 4 exponent and 3 fraction bits, largest 448 */
+#define GPT2_KV8_MAX_SEQS 4096 /* entries of one call */
+typedef struct {
+  int format;     /* GPT2_KV_INT8 or GPT2_KV_E4M3 */
+  int n_layer;    /* 1..1024 */
+  int n_kv_head;  /* 1..1024 */
+  int head_dim;   /* 64 or 128 */
+  int page_size;  /* tokens of a page: 16, 32, 64 or 128 */
+  int num_pages;  /* 1..2^24 */
+  int num_slots;  /* 1..65536 */
+  int max_pages;  /* table entries of a slot (max_pages * page_size <= 2^30) */
+  void* d_codes;    /* [num_pages][n_layer][2][n_kv_head][page_size][head_dim], 8 bits each, 16-byte aligned */
+  float* d_scales;  /* [num_pages][n_layer][2][n_kv_head] */
+  int32_t* d_table; /* [num_slots][max_pages] */
+  int32_t* d_lens;  /* [num_slots] */
+  int32_t* d_refs;  /* [num_pages] slots that hold the page (0: free), 16-byte aligned */
+} gpt2_kv8;
+
+/* Scratch of a resize, fork or compact with up to n entries (16-byte aligned). */
+size_t gpt2_kv8_workspace_bytes(const gpt2_kv8* cache, int n);
+/* d_slots[i] to the length d_new_lens[i], i < n <= GPT2_KV8_MAX_SEQS: longer
+ * slots get pages (their tokens are then written by gpt2_kv8_append), shorter
+ * ones give pages back, 0 frees the slot.  Pages given back are free for this
+ * call too; free pages are taken lowest id first, in the order of the list.
+ * A slot's last page that stays in use in part and that other slots share is
+ * first copied to a page of its own, so an unfinished page is never shared.
+ * Refused as a whole, changing nothing: a slot out of range or named twice, a
+ * length above max_pages * page_size, too few free pages. */
+int gpt2_kv8_resize(const gpt2_kv8* cache, const int32_t* d_slots, const int32_t* d_new_lens, int n, void* d_work,
+                    size_t work_bytes, void* cuda_stream);
+/* The empty slots d_dst[i] take over the tokens of d_src[i] (which may repeat):
+ * full pages are shared, an unfinished last page is copied to a free page
+ * (lowest id first, in the order of the list).  Refused as a whole, changing
+ * nothing: a slot out of range, a destination that is not empty or named
+ * twice, too few free pages. */
+int gpt2_kv8_fork(const gpt2_kv8* cache, const int32_t* d_src, const int32_t* d_dst, int n, void* d_work,
+                  size_t work_bytes, void* cuda_stream);
+/* Move the pages in use to the ids below their number: the j-th used page at
+ * or above it goes to the j-th free one below it; tables and counts follow.
+ * d_live (may be NULL) receives the number of pages in use: everything from
+ * that page on is then free and may be cut off or moved elsewhere. */
+int gpt2_kv8_compact(const gpt2_kv8* cache, int32_t* d_live, void* d_work, size_t work_bytes, void* cuda_stream);
+/* Round new keys and values of one layer into the cache.  d_k, d_v: bf16 rows
+ * of n_kv_head * head_dim values, `ld` elements apart (so the column blocks of
+ * a fused projection are read in place); ld a multiple of 8, pointers 16-byte
+ * aligned.  Rows d_cu[i] .. d_cu[i+1]-1 (d_cu: n + 1 non-decreasing offsets,
+ * at most `rows`) are the LAST tokens of slot d_slots[i], whose length already
+ * counts them (gpt2_kv8_resize first, once for all layers).
+ * The scale of a block is the smallest power of two (at least 2^-126) with
+ * which the largest magnitude among its tokens fits the codes' range; when a
+ * later token is larger, the block's codes are rounded once more to the grown
+ * scale.  Codes are rounded to nearest even.  A value that is not finite makes
+ * its block read as NaN.  A slot named twice (its later entries) or shorter
+ * than its rows is skipped and recorded (GPT2_ECACHE); offsets that decrease
+ * or pass `rows` refuse the whole call. */
+int gpt2_kv8_append(const gpt2_kv8* cache, int layer, const void* d_k, const void* d_v, int64_t ld,
+                    const int32_t* d_slots, const int32_t* d_cu, int n, int rows, void* cuda_stream);
+/* Scratch of gpt2_kv8_attention with these arguments (16-byte aligned); it needs no initialisation. */
+size_t gpt2_kv8_attention_workspace_bytes(const gpt2_kv8* cache, int n_head, int n, int rows, int max_q);
+/* Causal attention of the newest tokens over one layer of the cache, softmax
+ * scale 1/sqrt(head_dim).  d_q, d_out: bf16 rows of n_head * head_dim values,
+ * ldq / ldo elements apart (multiples of 8, pointers 16-byte aligned); query
+ * head j reads key/value head j / (n_head / n_kv_head); n_head is a multiple
+ * of n_kv_head, at most 64 times it.  d_slots, d_cu, n, rows as for
+ * gpt2_kv8_append: row r of slot s sees that slot's tokens up to its own.
+ * max_q: no sequence has more rows than this (host value; larger ones are
+ * skipped and recorded).  d_lse (may be NULL): fp32 [rows][n_head], natural
+ * log of the softmax denominators.  Rows that belong to no sequence, and those
+ * of a skipped one, are left as they were.  Deterministic: the same inputs on
+ * the same device give the same bits. */
+int gpt2_kv8_attention(const gpt2_kv8* cache, int layer, const void* d_q, int64_t ldq, void* d_out, int64_t ldo,
+                       float* d_lse, int n_head, const int32_t* d_slots, const int32_t* d_cu, int n, int rows,
+                       int max_q, void* d_work, size_t work_bytes, void* cuda_stream);
+
 /* ---- device-side errors of the standalone operators ----
  * The kernels never trap.  A pipeline wait that gives up (a producer or
  * consumer that did not arrive within the wait limit) records an error code
@@ -250,8 +345,9 @@ size_t gpt2_matmul_workspace_bytes(int M, int N, int K);
  * asynchronous and do not, so callers check it here:
  * gpt2_check_device_error synchronises cuda_stream (NULL = legacy default
  * stream), then reads and clears the error word of the current device.
- * Returns GPT2_OK when no kernel recorded an error since the last check, and
- * GPT2_ECUDA when one did (or the synchronisation failed).  The word is shared
+ * Returns GPT2_OK when no kernel recorded an error since the last check,
+ * GPT2_ECACHE when a paged-cache call was refused on the device, and
+ * GPT2_ECUDA otherwise (or when the synchronisation failed).  The word is shared
  * by every caller on the device: check before trusting a standalone result. */
 int gpt2_check_device_error(void* cuda_stream);
 /* Testing support: the time after which a device-side pipeline wait gives up,

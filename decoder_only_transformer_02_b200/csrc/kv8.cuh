@@ -27,6 +27,7 @@ constexpr int MAX_SEQS = 4096;      // entries of one call (their offsets are sc
 constexpr int MAX_SLOTS = 1 << 16;  // the duplicate check's bitmap is 8 KB of shared memory
 constexpr int MAX_PAGES = 1 << 24;
 constexpr int MAX_TOKENS = 1 << 30;  // of a slot
+constexpr int MAX_ROWS = 1 << 24;    // of a call
 constexpr uint32_t NAN_SCALE = 0x7fc00000u;
 
 struct Cache {

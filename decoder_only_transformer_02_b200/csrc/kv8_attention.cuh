@@ -2,118 +2,665 @@
 //
 // Sequence i of the call has len cached tokens, the last q_i = cu[i+1] - cu[i]
 // of which are the call's rows; the row at position p sees the tokens 0..p.
-// Query head j reads key/value head j / (n_head / n_kv_head).
-//   s_t = (q . kc_t) ks_t / sqrt(d)      kc, vc codes; ks, vs their pages' scales
+// Query head j reads key/value head j / group, group = n_head / n_kv_head.
+//   s_t = (q . kc_t) ks_t / sqrt(d)      kc, vc codes; ks, vs their blocks' scales
 //   p_t = exp(s_t - max)                 lse = max + log(sum p_t)
 //   o   = sum_t p_t vs_t vc_t / sum_t p_t
+//
+// For single tokens (and up to tens of rows per key/value head) the codes of
+// the cache are the traffic, 2 d bytes per token and head: the kernel streams
+// them once, straight from global memory into the registers that the matrix
+// instructions read, with no shared memory in between.
+//  - S^T = K Q^T and O^T = V^T P^T on mma m16n8k16 (f16 in, fp32 out), tokens
+//    (then dimensions) in the 16 rows and 8 query rows in the columns: with few
+//    rows this wastes half as much of an instruction as rows in the 16 would.
+//    (tcgen05's smallest tile has 64 rows and takes its operands from shared
+//    memory, 16 times the work of these products at one query row.)
+//  - A thread's 16 bytes of a key are its A operand: which dimension stands at
+//    which k index is free as long as Q agrees, so no code moves between lanes.
+//    The values' operand pairs two tokens of one dimension, a byte permute.
+//  - Codes become f16 exactly: e4m3 by its conversion instruction, int8 by
+//    placing the byte under 1024's exponent and subtracting 1152.  Q's rows are
+//    scaled by a power of two into f16's range (bf16 has fewer fraction bits,
+//    so this too is exact for components within 2^-29 of the row's largest).
+//  - Weights: p vs 2^6 / vref in f16 (2^-11 relative), vref the largest value
+//    scale seen, so that they stay below 2^14; sums, maxima, scores and O in fp32.
+//  - The row maximum moves only when a score passes it by 2^8 (one vote per
+//    step instead of a reduction over the lanes).
+//  - All sequences' 16-token groups, tile after tile (a tile: the rows of one
+//    sequence and key/value head), are one line of work that is cut into equal
+//    parts, one per CTA; a part's warps split each piece of a tile.  A tile
+//    that was cut leaves partial results that a second kernel joins in order,
+//    so the result is the same in every run.
 #pragma once
 #include "kv8.cuh"
 
 namespace kv8 {
 
-// One warp per (row, query head): 32 tokens at a time, one score per lane,
-// then the values with the lanes over the head's dimensions.
-template <int FMT, int D>
-__global__ void __launch_bounds__(128)
-    attention_kernel(Cache c, int layer, const bf16* __restrict__ q, long ldq, bf16* __restrict__ out, long ldo,
-                     float* __restrict__ lse, int H, const int32_t* __restrict__ slots, const int32_t* __restrict__ cu,
-                     int n, int rows, int max_q) {
-  const int lane = threadIdx.x & 31;
-  bool bad = false;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) bad |= cu[i] < 0 || cu[i + 1] < cu[i] || cu[i + 1] > rows;
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) set_device_err(DERR_KV8_ARGS);
-    return;
+constexpr int GROUP = 16;  // tokens of a step: one page, one matrix instruction's rows
+
+// ------------------------------------------------------------- instructions
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit elements held as mma fragments
+__device__ __forceinline__ uint32_t mat_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// four codes to two f16 pairs
+template <int FMT>
+__device__ __forceinline__ void codes_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == GPT2_KV_E4M3) {
+    lo = e4m3x2_to_half2(w & 0xffffu);
+    hi = e4m3x2_to_half2(w >> 16);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;  // code + 128
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));  // 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
   }
-  const long id = ((long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (id >= (long)rows * H) return;
-  const int row = (int)(id / H), h = (int)(id % H);
-  if (row < cu[0] || row >= cu[n]) return;
-  int lo = 0, hi = n;  // the sequence with cu[lo] <= row < cu[lo + 1]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (cu[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int a = cu[lo], b = cu[lo + 1], slot = slots[lo];
-  const int len = c.len_of(slot);
-  if (a > row || b <= row || len < b - a || b - a > max_q) {
-    if (lane == 0) set_device_err(DERR_KV8_ARGS);
-    return;
-  }
-  const int kvh = h / (H / c.kvh), last = len - (b - row);  // position of this row
-  const float sc = LOG2E_F / sqrtf((float)D);
-  float qv[D];
-#pragma unroll
-  for (int e = 0; e < D; ++e) qv[e] = bf2f(q[row * ldq + h * D + e]);
-  float m = -INFINITY, l = 0.f, o[D / 32];
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  for (int t0 = 0; t0 <= last; t0 += 32) {
-    const int t = t0 + lane;
-    float s = -INFINITY, vs = 0.f;
-    long vu = 0;
-    bool ok = true;
-    if (t <= last) {
-      const int page = c.table[(long)slot * c.max_pages + (t >> c.ps_log2)];
-      ok = c.page_ok(page);
-      if (ok) {
-        const long ku = c.unit(page, layer, 0, kvh);
-        vu = c.unit(page, layer, 1, kvh);
-        const uint32_t* kr = reinterpret_cast<const uint32_t*>(c.codes + ku * c.tile() + (long)(t & (c.ps - 1)) * D);
-        float acc = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) {
-          float f[4];
-          unpack4<FMT>(kr[e], f);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) acc = fmaf(f[g], qv[4 * e + g], acc);
-        }
-        s = acc * c.scales[ku] * sc;
-        vs = c.scales[vu];
-      }
-    }
-    if (__any_sync(0xffffffffu, !ok)) {
-      if (lane == 0) set_device_err(DERR_KV8_TABLE);
-      return;
-    }
-    const float nm = fmaxf(m, warp_max(s)), alpha = exp2f(m - nm), p = t <= last ? exp2f(s - nm) : 0.f;
-    m = nm;
-    l = l * alpha + warp_sum(p);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] *= alpha;
-    const int cnt = min(32, last + 1 - t0);
-    for (int j = 0; j < cnt; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, p * vs, j);
-      const long u = __shfl_sync(0xffffffffu, vu, j);
-      const uint8_t* vr = c.codes + u * c.tile() + (long)((t0 + j) & (c.ps - 1)) * D;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        float f[4];
-        unpack4<FMT>(vr[e * 32 + lane], f);
-        o[e] = fmaf(pj, f[0], o[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) out[row * ldo + h * D + e * 32 + lane] = f2bf(o[e] / l);
-  if (lane == 0 && lse) lse[(long)row * H + h] = (m + log2f(l)) * 0.6931471805599453f;
+}
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_stream(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
 
-static inline size_t attention_workspace_bytes(const Cache&, int, int, int, int) { return 256; }
+// ------------------------------------------------------------- the work line
+struct Call {
+  Cache c;
+  int layer, H, group, n, rows, max_q;
+  const bf16* q;
+  long ldq;
+  bf16* out;
+  long ldo;
+  float* lse;
+  const int32_t *slots, *cu;
+  float* part;   // [grid][2][rows of a tile][d + 2]
+  int min_part;  // fewest groups of a CTA's part
+};
+
+struct Entry {
+  int slot, len, a, q;  // q = 0: nothing to do (or skipped)
+};
+__device__ __forceinline__ Entry entry_of(const Call& k, int i) {
+  Entry e;
+  e.a = k.cu[i];
+  e.q = k.cu[i + 1] - e.a;
+  e.slot = k.slots[i];
+  e.len = 0;
+  if (e.q > 0) {
+    e.len = k.c.len_of(e.slot);
+    if (e.len < e.q || e.q > k.max_q) e.q = 0, e.len = -1;
+  }
+  return e;
+}
+// tiles of a sequence: kvh for every row_tile rows of (token, head of the group)
+__device__ __forceinline__ int row_tiles(const Call& k, int q, int row_tile) {
+  return (int)(((long)q * k.group + row_tile - 1) / row_tile);
+}
+
+// pre[i] = 16-token groups of all tiles before sequence i, pre[n] the total;
+// false when the offsets are bad (the call is refused).
+__device__ __forceinline__ bool lay_out(const Call& k, int row_tile, long long* pre, long long* s_warp, bool report) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long base = 0;
+  bool bad = false, skipped = false;
+  for (int i0 = 0; i0 < k.n; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    long long x = 0;
+    if (i < k.n) {
+      const int a = k.cu[i], b = k.cu[i + 1];
+      bad |= a < 0 || b < a || b > k.rows;
+      const Entry e = entry_of(k, i);
+      skipped |= e.len < 0;
+      if (e.q > 0) x = (long long)k.c.kvh * row_tiles(k, e.q, row_tile) * ((e.len + GROUP - 1) / GROUP);
+    }
+    const long long own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long before = base;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += s_warp[w];
+      base += s_warp[w];
+    }
+    if (i < k.n) pre[i] = before + x - own;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[k.n] = base;
+  if (skipped && report) set_device_err(DERR_KV8_ARGS);
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0 && report) set_device_err(DERR_KV8_ARGS);
+    return false;
+  }
+  return true;
+}
+// groups of one CTA's part
+__device__ __forceinline__ long long part_size(long long total, int grid, int least) {
+  const long long p = (total + grid - 1) / grid;
+  return p < least ? least : p;
+}
+
+struct Piece {
+  Entry e;
+  int head, row0, g0, g1, groups;  // key/value head, first row, groups [g0, g1) of `groups`
+};
+// the tile that holds group `at` of the line, and its groups up to `end`
+__device__ __forceinline__ Piece piece_at(const Call& k, const long long* pre, int row_tile, long long at, long long end) {
+  int lo = 0, hi = k.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= at) lo = mid; else hi = mid;
+  }
+  Piece p;
+  p.e = entry_of(k, lo);
+  p.groups = (p.e.len + GROUP - 1) / GROUP;
+  const long long rel = at - pre[lo];
+  const int tile = (int)(rel / p.groups);
+  p.g0 = (int)(rel - (long long)tile * p.groups);
+  p.g1 = (int)min((long long)p.groups, p.g0 + (end - at));
+  p.head = tile % k.c.kvh;
+  p.row0 = (tile / k.c.kvh) * row_tile;
+  return p;
+}
+
+// --------------------------------------------------------- streaming kernel
+constexpr int S_WARPS = 4;
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(32 * S_WARPS, NT * D <= 64 ? 4 : NT * D <= 128 ? 3 : 2) stream_kernel(const Call k) {
+  constexpr int RT = 8 * NT;           // rows of a tile
+  constexpr int CH = D / 64;           // 16-byte pieces of a key per thread
+  constexpr int U = D == 64 ? 2 : 1;   // groups per step (4 KB of codes per warp and step)
+  constexpr int VW = D / 32;           // 4-byte words of a value per thread and token
+  extern __shared__ long long s_dyn[];
+  __shared__ long long s_warp[S_WARPS];
+  __shared__ float s_m[S_WARPS][RT], s_l[S_WARPS][RT];
+  float* s_o = reinterpret_cast<float*>(s_dyn);  // [S_WARPS][RT][D]
+  long long* pre = s_dyn + S_WARPS * RT * D / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, tg = lane & 3;
+  const Cache& c = k.c;
+  pdl_launch();
+  if (!lay_out(k, RT, pre, s_warp, blockIdx.x == 0)) return;
+  const long long total = pre[k.n], per = part_size(total, gridDim.x, k.min_part);
+  long long at = blockIdx.x * per;
+  const long long end = min(total, at + per);
+  const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
+
+  while (at < end) {
+    const Piece p = piece_at(k, pre, RT, at, end);
+    at += p.g1 - p.g0;
+    const int tile_rows = min(RT, p.e.q * k.group - p.row0);
+    // ---- Q: row g of each n tile, dimensions 64 c + 16 tg .. + 15
+    uint32_t qb[NT][CH][8];
+    float rowf[NT][2];  // score factor of rows 2 tg, 2 tg + 1
+    int minpos = p.e.len;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = p.row0 + nt * 8 + g;
+      const bool on = nt * 8 + g < tile_rows;
+      const int tok = on ? r / k.group : 0;
+      const bf16* src = k.q + (long)(p.e.a + tok) * k.ldq + (p.head * k.group + (on ? r - tok * k.group : 0)) * D + 16 * tg;
+      uint32_t raw[CH][8], mx = 0;
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (on) {
+          x = *reinterpret_cast<const uint4*>(src + 64 * ch);
+          y = *reinterpret_cast<const uint4*>(src + 64 * ch + 8);
+        }
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          raw[ch][e] = w[e];
+          mx = __vmaxu2(mx, w[e] & 0x7fff7fffu);
+        }
+      }
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // times 2^(14 - exponent of the largest), at most 2^126
+      const int E = max((int)(mx >> 7), 15);
+      const float up = __uint_as_float((uint32_t)(268 - E) << 23), down = __uint_as_float((uint32_t)(E - 14) << 23);
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = unpack_bf16x2(raw[ch][e]);
+          qb[nt][ch][e] = half2_of(f.x * up, f.y * up);
+        }
+      rowf[nt][0] = __shfl_sync(0xffffffffu, down, 8 * tg) * sl2;
+      rowf[nt][1] = __shfl_sync(0xffffffffu, down, 8 * tg + 4) * sl2;
+    }
+    // positions: row r's token sees tokens <= len - q + r / group
+    const int pos0 = p.e.len - p.e.q;
+    minpos = pos0 + p.row0 / k.group;
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) pos[nt][j] = pos0 + (p.row0 + nt * 8 + 2 * tg + j) / k.group;
+
+    float o[D / 16][NT][4], m[NT][2], mu[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      mu[nt][0] = mu[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    }
+    float vref = 0.f, vinv = 0.f;
+
+    // ---- this warp's groups
+    const int cnt = p.g1 - p.g0;
+    const int gs = p.g0 + (int)((long)cnt * warp / S_WARPS), ge = p.g0 + (int)((long)cnt * (warp + 1) / S_WARPS);
+    const int32_t* table = c.table + (long)p.e.slot * c.max_pages;
+    const int gp_log2 = c.ps_log2 - 4;  // groups of a page
+    // lane x holds the page and scales of group base + x
+    int pg = 0;
+    float ksc = 0.f, vsc = 0.f;
+    auto batch = [&](int base) {
+      const int gi = base + lane;
+      pg = 0;
+      ksc = vsc = 0.f;
+      if (gi < ge) {
+        pg = table[gi >> gp_log2];
+        if (c.page_ok(pg)) {
+          ksc = c.scales[c.unit(pg, k.layer, 0, p.head)];
+          vsc = c.scales[c.unit(pg, k.layer, 1, p.head)];
+        } else {
+          set_device_err(DERR_KV8_TABLE);
+          pg = 0;
+          ksc = vsc = __uint_as_float(NAN_SCALE);
+        }
+      }
+    };
+    uint32_t kw[U][2][CH][4], vw[U][4][VW];
+    float ksn[U], vsn[U];
+    const int tile_bytes = c.ps * D;
+    const long page_stride = c.page_bytes();
+    const uint8_t* head_base = c.codes + ((long)k.layer * 2 * c.kvh + p.head) * tile_bytes;
+    const long side_stride = (long)c.kvh * tile_bytes;
+    int base = gs;
+    auto load = [&](int gi) {  // groups gi .. gi + U - 1 into kw, vw
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int page = __shfl_sync(0xffffffffu, pg, (gi + u - base) & 31);
+        ksn[u] = __shfl_sync(0xffffffffu, ksc, (gi + u - base) & 31);
+        vsn[u] = __shfl_sync(0xffffffffu, vsc, (gi + u - base) & 31);
+        if (gi + u < ge) {
+          const uint8_t* t = head_base + page * page_stride + (((gi + u) << 4) & (c.ps - 1)) * D;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+              const uint4 x = ld_stream(reinterpret_cast<const uint4*>(t + (g + 8 * h) * D + 64 * ch + 16 * tg));
+              kw[u][h][ch][0] = x.x, kw[u][h][ch][1] = x.y, kw[u][h][ch][2] = x.z, kw[u][h][ch][3] = x.w;
+            }
+          t += side_stride;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint8_t* s = t + (2 * tg + (e & 1) + 8 * (e >> 1)) * D + (D / 8) * g;
+            if (D == 64) {
+              const uint2 x = ld_stream(reinterpret_cast<const uint2*>(s));
+              vw[u][e][0] = x.x, vw[u][e][1] = x.y;
+            } else {
+              const uint4 x = ld_stream(reinterpret_cast<const uint4*>(s));
+              vw[u][e][0] = x.x, vw[u][e][1] = x.y, vw[u][e][VW - 2] = x.z, vw[u][e][VW - 1] = x.w;
+            }
+          }
+        }
+      }
+    };
+    auto new_batch = [&](int at_group) {
+      base = at_group;
+      batch(base);
+      // the largest value scale so far (NaN scales, as negative integers or none, do not take part)
+      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, vsc <= 3.0e38f ? __float_as_uint(fabsf(vsc)) : 0u));
+      if (top > vref) {
+        const float f = vref > 0.f ? vref / top : 0.f;
+        if (vref > 0.f) {
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f;
+        }
+        vref = top;
+        vinv = 1.f / top;
+      }
+    };
+    if (gs < ge) {
+      new_batch(gs);
+      load(gs);
+    }
+    for (int gi = gs; gi < ge; gi += U) {
+      // this step's codes; the next step's loads go out before its arithmetic
+      uint32_t kc[U][2][CH][4], vc[U][4][VW];
+      float ks[U], vs[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ks[u] = ksn[u];
+        vs[u] = vsn[u];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kc[u][h][ch][e] = kw[u][h][ch][e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vc[u][e][w] = vw[u][e][w];
+      }
+      if (gi + U < ge) {
+        if (gi + U - base >= 32) new_batch(gi + U);
+        load(gi + U);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) vs[u] = vs[u] * vinv * 64.f;
+      // ---- scores
+      float s[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            codes_half<FMT>(kc[u][0][ch][w], a0, a2);
+            codes_half<FMT>(kc[u][1][ch][w], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][ch][2 * w], qb[nt][ch][2 * w + 1]);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f0 = ks[u] * rowf[nt][0], f1 = ks[u] * rowf[nt][1];
+          s[u][nt][0] *= f0;
+          s[u][nt][1] *= f1;
+          s[u][nt][2] *= f0;
+          s[u][nt][3] *= f1;
+        }
+      }
+      const int t0 = gi * GROUP;
+      const bool edge = t0 + U * GROUP - 1 > minpos || gi + U > ge;
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gi + u >= ge || t0 + u * GROUP + g + 8 * (e >> 1) > pos[nt][e & 1]) s[u][nt][e] = -INFINITY;
+          // values behind the last token may hold anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (gi + u >= ge || t0 + u * GROUP + 2 * tg + (e & 1) + 8 * (e >> 1) >= p.e.len) {
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vc[u][e][w] = 0;
+            }
+        }
+      }
+      // ---- row maxima, moved only past 2^8
+      float top[NT][2];
+      bool past = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+          for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][nt][j], s[u][nt][j + 2]));
+          top[nt][j] = x;
+          past |= x > m[nt][j] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = top[nt][j];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float nm = fmaxf(m[nt][j], x);
+            al[j] = m[nt][j] == -INFINITY ? 0.f : ex2_approx(m[nt][j] - nm);
+            m[nt][j] = nm;
+            mu[nt][j] = nm == -INFINITY ? 0.f : nm;
+            l[nt][j] *= al[j];
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[mt][nt][0] *= al[0];
+            o[mt][nt][1] *= al[1];
+            o[mt][nt][2] *= al[0];
+            o[mt][nt][3] *= al[1];
+          }
+        }
+      }
+      // ---- weights, and the values' products
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = ex2_approx(s[u][nt][e] - mu[nt][e & 1]);
+            l[nt][e & 1] += x;
+            w[e] = x * vs[u];
+            if (edge && s[u][nt][e] == -INFINITY) w[e] = 0.f;  // also where the scale is NaN
+          }
+          pb[nt][0] = mat_trans(half2_of(w[0], w[1]));
+          pb[nt][1] = mat_trans(half2_of(w[2], w[3]));
+        }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          uint32_t a0, a1, a2, a3;
+          const int sel = mt & 1 ? 0x7362 : 0x5140;
+          codes_half<FMT>(__byte_perm(vc[u][0][mt >> 1], vc[u][1][mt >> 1], sel), a0, a1);
+          codes_half<FMT>(__byte_perm(vc[u][2][mt >> 1], vc[u][3][mt >> 1], sel), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      }
+    }
+    // ---- the warps' results joined in shared memory
+    const float unit = vref * (1.f / 64.f);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = l[nt][j];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int r = nt * 8 + 2 * tg + j;
+        if (g == 0) {
+          s_m[warp][r] = m[nt][j];
+          s_l[warp][r] = x;
+        }
+        float* dst = s_o + ((long)warp * RT + r) * D + (D / 8) * g;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; mt += 2)
+          *reinterpret_cast<float4*>(dst + 2 * mt) =
+              make_float4(o[mt][nt][j] * unit, o[mt][nt][j + 2] * unit, o[mt + 1][nt][j] * unit, o[mt + 1][nt][j + 2] * unit);
+      }
+    __syncthreads();
+    const bool whole = p.g0 == 0 && p.g1 == p.groups;
+    float* part = k.part + ((long)blockIdx.x * 2 + (p.g0 == 0)) * RT * (D + 2);
+    for (int i = threadIdx.x; i < tile_rows * (D / 4); i += 32 * S_WARPS) {
+      const int r = i / (D / 4), d4 = i % (D / 4);
+      float M = s_m[0][r], L = 0.f;
+#pragma unroll
+      for (int w = 1; w < S_WARPS; ++w) M = fmaxf(M, s_m[w][r]);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < S_WARPS; ++w) {
+        const float f = ex2_approx(s_m[w][r] - Mu);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + ((long)w * RT + r) * D + 4 * d4);
+        L += f * s_l[w][r];
+        a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = 1.f / L;
+        const int row = p.row0 + r, tok = row / k.group, h = p.head * k.group + row - tok * k.group;
+        *reinterpret_cast<uint2*>(k.out + (long)(p.e.a + tok) * k.ldo + h * D + 4 * d4) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (d4 == 0 && k.lse) k.lse[(long)(p.e.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(part + r * D + 4 * d4) = a;
+        if (d4 == 0) {
+          part[RT * D + r] = M;
+          part[RT * D + RT + r] = L;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// CTA x joins the tile that began in part x of the line and went on past it:
+// its partial results lie with part x (place 1) and the parts after it (place 0).
+template <int D, int RT>
+__global__ void __launch_bounds__(128) join_kernel(const Call k) {
+  extern __shared__ long long pre[];
+  __shared__ long long s_warp[4];
+  const bool ok = lay_out(k, RT, pre, s_warp, false);
+  pdl_wait();
+  if (!ok) return;
+  const long long total = pre[k.n], per = part_size(total, gridDim.x, k.min_part);
+  const long long begin = blockIdx.x * per, end = min(total, begin + per);
+  if (begin >= total || end >= total) return;
+  Piece p = piece_at(k, pre, RT, end - 1, end);  // the tile of the part's last group
+  const long long tile0 = end - 1 - p.g0, tile1 = tile0 + p.groups;
+  if (tile0 < begin || tile1 <= end) return;     // began earlier, or is whole
+  const int parts = (int)((tile1 - 1) / per) - blockIdx.x + 1;
+  const int tile_rows = min(RT, p.e.q * k.group - p.row0);
+  constexpr long STEP = 2L * RT * (D + 2);
+  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * RT * (D + 2);
+  for (int i = threadIdx.x; i < tile_rows * (D / 4); i += 128) {
+    const int r = i / (D / 4), d4 = i % (D / 4);
+    float M = first[RT * D + r];
+    for (int j = 1; j < parts; ++j) M = fmaxf(M, first[j * STEP - RT * (D + 2) + RT * D + r]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < parts; ++j) {
+      const float* src = first + (j ? j * STEP - RT * (D + 2) : 0);
+      const float f = ex2_approx(src[RT * D + r] - Mu);
+      const float4 x = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
+      L += f * src[RT * D + RT + r];
+      a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+    }
+    const float inv = 1.f / L;
+    const int row = p.row0 + r, tok = row / k.group, h = p.head * k.group + row - tok * k.group;
+    *reinterpret_cast<uint2*>(k.out + (long)(p.e.a + tok) * k.ldo + h * D + 4 * d4) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (d4 == 0 && k.lse) k.lse[(long)(p.e.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+static inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n > 0 ? n : 148;
+}
+
+// rows of a tile: the call's rows per key/value head, 8 to 32 (16 at d = 128)
+static inline int row_tile_of(const Cache& c, int group, int max_q) {
+  const long r = (long)group * max_q;
+  return r <= 8 ? 8 : r <= 16 || c.d == 128 ? 16 : 32;
+}
+static inline int ctas_per_sm(const Cache& c, int rt) { return rt * c.d <= 512 ? 4 : rt * c.d <= 1024 ? 3 : 2; }
+
+static inline size_t attention_workspace_bytes(const Cache& c, int H, int, int, int max_q) {
+  const int rt = row_tile_of(c, H / c.kvh, max_q);
+  return (size_t)sm_count() * ctas_per_sm(c, rt) * 2 * rt * (c.d + 2) * 4;
+}
+
+template <int FMT, int D, int NT>
+static inline cudaError_t stream_launch(const Call& k, cudaStream_t st) {
+  constexpr int RT = 8 * NT;
+  const size_t pre = (size_t)(k.n + 1) * 8, smem = pre + (size_t)S_WARPS * RT * D * 4;
+  static DeviceOnce once;
+  cudaError_t e = run_once_per_device(once, [] {
+    cudaError_t r = cudaFuncSetAttribute(stream_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (MAX_SEQS + 1) * 8 + S_WARPS * RT * D * 4);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count() * ctas_per_sm(k.c, RT);
+  stream_kernel<FMT, D, NT><<<grid, 32 * S_WARPS, smem, st>>>(k);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(join_kernel<D, RT>, dim3(grid), 128, pre, st, k);
+}
+template <int FMT>
+static inline cudaError_t stream_rows(const Call& k, cudaStream_t st) {
+  const int rt = row_tile_of(k.c, k.group, k.max_q);
+  if (k.c.d == 64)
+    return rt == 8 ? stream_launch<FMT, 64, 1>(k, st) : rt == 16 ? stream_launch<FMT, 64, 2>(k, st) : stream_launch<FMT, 64, 4>(k, st);
+  return rt == 8 ? stream_launch<FMT, 128, 1>(k, st) : stream_launch<FMT, 128, 2>(k, st);
+}
 
 static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, long ldq, bf16* out, long ldo,
                                     float* lse, int H, const int32_t* slots, const int32_t* cu, int n, int rows,
                                     int max_q, void* work, cudaStream_t st) {
-  (void)work;
-  if (n == 0 || rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)(((long)rows * H + 3) / 4);
-#define KV8_GO(F, D_) attention_kernel<F, D_><<<grid, 128, 0, st>>>(c, layer, q, ldq, out, ldo, lse, H, slots, cu, n, rows, max_q)
-  if (c.fmt == GPT2_KV_INT8)
-    c.d == 64 ? KV8_GO(GPT2_KV_INT8, 64) : KV8_GO(GPT2_KV_INT8, 128);
-  else
-    c.d == 64 ? KV8_GO(GPT2_KV_E4M3, 64) : KV8_GO(GPT2_KV_E4M3, 128);
-#undef KV8_GO
-  return cudaGetLastError();
+  Call k;
+  k.c = c;
+  k.layer = layer;
+  k.H = H;
+  k.group = H / c.kvh;
+  k.n = n;
+  k.rows = rows;
+  k.max_q = max_q;
+  k.q = q;
+  k.ldq = ldq;
+  k.out = out;
+  k.ldo = ldo;
+  k.lse = lse;
+  k.slots = slots;
+  k.cu = cu;
+  k.part = static_cast<float*>(work);
+  k.min_part = 2 * S_WARPS;
+  return c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, st) : stream_rows<GPT2_KV_E4M3>(k, st);
 }
 
 }  // namespace kv8

@@ -432,7 +432,7 @@ static bool kv8_work_ok(const kv8::Cache& c, int n, const void* work, size_t byt
 }
 
 static bool kv8_counts_ok(int n, int rows) {
-  return n >= 0 && n <= GPT2_KV8_MAX_SEQS && rows >= 0 && rows <= kv8::MAX_TOKENS;
+  return n >= 0 && n <= GPT2_KV8_MAX_SEQS && rows >= 0 && rows <= kv8::MAX_ROWS;
 }
 // rows of `width` elements, `ld` apart
 static bool kv8_ptr_ok(const void* p, int64_t ld, long width) {

@@ -308,7 +308,7 @@ int gpt2_kv8_compact(const gpt2_kv8* cache, int32_t* d_live, void* d_work, size_
  * of n_kv_head * head_dim values, `ld` elements apart (so the column blocks of
  * a fused projection are read in place); ld a multiple of 8, pointers 16-byte
  * aligned.  Rows d_cu[i] .. d_cu[i+1]-1 (d_cu: n + 1 non-decreasing offsets,
- * at most `rows`) are the LAST tokens of slot d_slots[i], whose length already
+ * at most `rows` <= 2^24) are the LAST tokens of slot d_slots[i], whose length already
  * counts them (gpt2_kv8_resize first, once for all layers).
  * The scale of a block is the smallest power of two (at least 2^-126) with
  * which the largest magnitude among its tokens fits the codes' range; when a
@@ -330,7 +330,8 @@ size_t gpt2_kv8_attention_workspace_bytes(const gpt2_kv8* cache, int n_head, int
  * max_q: no sequence has more rows than this (host value; larger ones are
  * skipped and recorded).  d_lse (may be NULL): fp32 [rows][n_head], natural
  * log of the softmax denominators.  Rows that belong to no sequence, and those
- * of a skipped one, are left as they were.  Deterministic: the same inputs on
+ * of a skipped one, are left as they were; where the page table holds an id
+ * outside the pool (recorded), the rows that read it are NaN.  Deterministic: the same inputs on
  * the same device give the same bits. */
 int gpt2_kv8_attention(const gpt2_kv8* cache, int layer, const void* d_q, int64_t ldq, void* d_out, int64_t ldo,
                        float* d_lse, int n_head, const int32_t* d_slots, const int32_t* d_cu, int n, int rows,

@@ -83,6 +83,7 @@ __device__ __forceinline__ uint2 ld_stream(const uint2* p) {
 }
 
 // ------------------------------------------------------------- the work line
+struct Join;
 struct Call {
   Cache c;
   int layer, H, group, n, rows, max_q;
@@ -92,45 +93,55 @@ struct Call {
   long ldo;
   float* lse;
   const int32_t *slots, *cu;
-  float* part;   // [grid][2][rows of a tile][d + 2]
-  int min_part;  // fewest groups of a CTA's part
+  Join* join;         // [grid]
+  float* part;        // [grid][2][rows of a tile][d + 2]
+  int setup;          // units of the line that beginning a tile counts
+  int min_part;       // fewest units of a CTA's part
 };
 
 struct Entry {
-  int slot, len, a, q;  // q = 0: nothing to do (or skipped)
+  int slot, len, a, q;  // q = 0: nothing to do
 };
-__device__ __forceinline__ Entry entry_of(const Call& k, int i) {
-  Entry e;
-  e.a = k.cu[i];
-  e.q = k.cu[i + 1] - e.a;
-  e.slot = k.slots[i];
-  e.len = 0;
-  if (e.q > 0) {
-    e.len = k.c.len_of(e.slot);
-    if (e.len < e.q || e.q > k.max_q) e.q = 0, e.len = -1;
-  }
-  return e;
-}
 // tiles of a sequence: kvh for every row_tile rows of (token, head of the group)
 __device__ __forceinline__ int row_tiles(const Call& k, int q, int row_tile) {
   return (int)(((long)q * k.group + row_tile - 1) / row_tile);
 }
+__device__ __forceinline__ int groups_of(int len) { return (len + GROUP - 1) / GROUP; }
 
-// pre[i] = 16-token groups of all tiles before sequence i, pre[n] the total;
-// false when the offsets are bad (the call is refused).
-__device__ __forceinline__ bool lay_out(const Call& k, int row_tile, long long* pre, long long* s_warp, bool report) {
+// A tile takes its 16-token groups and `setup` units more on the line, what
+// beginning one costs in groups.
+struct Line {
+  long long* pre;  // [n + 1] units before each sequence
+  int4* entry;     // [n] Entry
+  int setup;
+  static __host__ __device__ size_t bytes(int n) { return (size_t)n * 16 + (size_t)(n + 1) * 8; }
+  __device__ Line(void* smem, int n, int setup_)
+      : pre(reinterpret_cast<long long*>(static_cast<int4*>(smem) + n)), entry(static_cast<int4*>(smem)), setup(setup_) {}
+};
+
+// Fills the line; false when the offsets are bad (the call is refused).
+__device__ __forceinline__ bool lay_out(const Call& k, int row_tile, const Line& line, long long* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const bool report = blockIdx.x == 0;
   long long base = 0;
-  bool bad = false, skipped = false;
+  bool bad = false;
   for (int i0 = 0; i0 < k.n; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
     long long x = 0;
     if (i < k.n) {
-      const int a = k.cu[i], b = k.cu[i + 1];
+      const int a = k.cu[i], b = k.cu[i + 1], slot = k.slots[i];
       bad |= a < 0 || b < a || b > k.rows;
-      const Entry e = entry_of(k, i);
-      skipped |= e.len < 0;
-      if (e.q > 0) x = (long long)k.c.kvh * row_tiles(k, e.q, row_tile) * ((e.len + GROUP - 1) / GROUP);
+      int q = b - a, len = 0;
+      if (q > 0) {
+        len = k.c.len_of(slot);
+        if (len < q || q > k.max_q) {
+          q = 0;
+          if (report) set_device_err(DERR_KV8_ARGS);
+        } else {
+          x = (long long)k.c.kvh * row_tiles(k, q, row_tile) * (groups_of(len) + line.setup);
+        }
+      }
+      line.entry[i] = make_int4(slot, len, a, q);
     }
     const long long own = x;
 #pragma unroll
@@ -145,45 +156,50 @@ __device__ __forceinline__ bool lay_out(const Call& k, int row_tile, long long* 
       if (w < warp) before += s_warp[w];
       base += s_warp[w];
     }
-    if (i < k.n) pre[i] = before + x - own;
+    if (i < k.n) line.pre[i] = before + x - own;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[k.n] = base;
-  if (skipped && report) set_device_err(DERR_KV8_ARGS);
+  if (threadIdx.x == 0) line.pre[k.n] = base;
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0 && report) set_device_err(DERR_KV8_ARGS);
     return false;
   }
   return true;
 }
-// groups of one CTA's part
-__device__ __forceinline__ long long part_size(long long total, int grid, int least) {
-  const long long p = (total + grid - 1) / grid;
-  return p < least ? least : p;
-}
 
 struct Piece {
   Entry e;
   int head, row0, g0, g1, groups;  // key/value head, first row, groups [g0, g1) of `groups`
+  long long next;                  // where the line goes on
 };
-// the tile that holds group `at` of the line, and its groups up to `end`
-__device__ __forceinline__ Piece piece_at(const Call& k, const long long* pre, int row_tile, long long at, long long end) {
+// the tile that holds unit `at` of the line, and its groups up to `end`
+__device__ __forceinline__ Piece piece_at(const Call& k, const Line& line, int row_tile, long long at, long long end) {
   int lo = 0, hi = k.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= at) lo = mid; else hi = mid;
+    if (line.pre[mid] <= at) lo = mid; else hi = mid;
   }
   Piece p;
-  p.e = entry_of(k, lo);
-  p.groups = (p.e.len + GROUP - 1) / GROUP;
-  const long long rel = at - pre[lo];
-  const int tile = (int)(rel / p.groups);
-  p.g0 = (int)(rel - (long long)tile * p.groups);
-  p.g1 = (int)min((long long)p.groups, p.g0 + (end - at));
+  const int4 e = line.entry[lo];
+  p.e.slot = e.x, p.e.len = e.y, p.e.a = e.z, p.e.q = e.w;
+  p.groups = groups_of(p.e.len);
+  const int size = p.groups + line.setup;
+  const long long rel = at - line.pre[lo];
+  const int tile = (int)(rel / size);
+  const int u = (int)(rel - (long long)tile * size);
+  p.next = min(at - u + size, end);
+  p.g0 = max(0, u - line.setup);
+  p.g1 = max(0, (int)(p.next - at) + u - line.setup);
   p.head = tile % k.c.kvh;
   p.row0 = (tile / k.c.kvh) * row_tile;
   return p;
 }
+
+// What is left to join: the tile that begins in part x and goes on in the next
+// parts (parts = 0: none).  Written by every CTA for its own x.
+struct Join {
+  int parts, tile_rows, row0, head, a, pad[3];
+};
 
 // --------------------------------------------------------- streaming kernel
 constexpr int S_WARPS = 4;
@@ -198,21 +214,32 @@ __global__ void __launch_bounds__(32 * S_WARPS, NT * D <= 64 ? 4 : NT * D <= 128
   __shared__ long long s_warp[S_WARPS];
   __shared__ float s_m[S_WARPS][RT], s_l[S_WARPS][RT];
   float* s_o = reinterpret_cast<float*>(s_dyn);  // [S_WARPS][RT][D]
-  long long* pre = s_dyn + S_WARPS * RT * D / 2;
+  const Line line(s_dyn + S_WARPS * RT * D / 2, k.n, k.setup);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tg = lane & 3;
   const Cache& c = k.c;
   pdl_launch();
-  if (!lay_out(k, RT, pre, s_warp, blockIdx.x == 0)) return;
-  const long long total = pre[k.n], per = part_size(total, gridDim.x, k.min_part);
+  const bool ok = lay_out(k, RT, line, s_warp);
+  const long long total = ok ? line.pre[k.n] : 0;
+  const long long per = max((long long)k.min_part, (total + gridDim.x - 1) / gridDim.x);
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
+  int join_parts = 0;
   const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
 
   while (at < end) {
-    const Piece p = piece_at(k, pre, RT, at, end);
-    at += p.g1 - p.g0;
+    const Piece p = piece_at(k, line, RT, at, end);
     const int tile_rows = min(RT, p.e.q * k.group - p.row0);
+    if (p.g0 == 0 && p.g1 > 0 && p.g1 < p.groups) {
+      join_parts = (int)((p.next + p.groups - p.g1 - 1) / per) - blockIdx.x + 1;
+      if (threadIdx.x == 0) {
+        Join j;
+        j.parts = join_parts, j.tile_rows = tile_rows, j.row0 = p.row0, j.head = p.head, j.a = p.e.a;
+        k.join[blockIdx.x] = j;
+      }
+    }
+    at = p.next;
+    if (p.g1 == p.g0) continue;  // only the tile's setup units are in this part
     // ---- Q: row g of each n tile, dimensions 64 c + 16 tg .. + 15
     uint32_t qb[NT][CH][8];
     float rowf[NT][2];  // score factor of rows 2 tg, 2 tg + 1
@@ -551,46 +578,65 @@ __global__ void __launch_bounds__(32 * S_WARPS, NT * D <= 64 ? 4 : NT * D <= 128
     }
     __syncthreads();
   }
+  if (join_parts == 0 && threadIdx.x == 0) k.join[blockIdx.x].parts = 0;
 }
 
 // CTA x joins the tile that began in part x of the line and went on past it:
-// its partial results lie with part x (place 1) and the parts after it (place 0).
+// its partial results lie with part x (place 1) and the parts after it (place
+// 0).  The warps take the parts in turn; results meet in warp order.
+constexpr int J_WARPS = 8;
 template <int D, int RT>
-__global__ void __launch_bounds__(128) join_kernel(const Call k) {
-  extern __shared__ long long pre[];
-  __shared__ long long s_warp[4];
-  const bool ok = lay_out(k, RT, pre, s_warp, false);
+__global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
+  constexpr int LANES = D / 4;  // threads of a row
+  __shared__ float4 s_a[J_WARPS][32];
+  __shared__ float s_m[J_WARPS][32], s_l[J_WARPS][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  if (!ok) return;
-  const long long total = pre[k.n], per = part_size(total, gridDim.x, k.min_part);
-  const long long begin = blockIdx.x * per, end = min(total, begin + per);
-  if (begin >= total || end >= total) return;
-  Piece p = piece_at(k, pre, RT, end - 1, end);  // the tile of the part's last group
-  const long long tile0 = end - 1 - p.g0, tile1 = tile0 + p.groups;
-  if (tile0 < begin || tile1 <= end) return;     // began earlier, or is whole
-  const int parts = (int)((tile1 - 1) / per) - blockIdx.x + 1;
-  const int tile_rows = min(RT, p.e.q * k.group - p.row0);
-  constexpr long STEP = 2L * RT * (D + 2);
-  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * RT * (D + 2);
-  for (int i = threadIdx.x; i < tile_rows * (D / 4); i += 128) {
-    const int r = i / (D / 4), d4 = i % (D / 4);
-    float M = first[RT * D + r];
-    for (int j = 1; j < parts; ++j) M = fmaxf(M, first[j * STEP - RT * (D + 2) + RT * D + r]);
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
+  const Join t = k.join[blockIdx.x];
+  if (t.parts == 0) return;
+  constexpr long SIZE = (long)RT * (D + 2);
+  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
+  for (int r0 = 0; r0 < t.tile_rows; r0 += 32 / LANES) {
+    const int r = r0 + lane / LANES, d4 = lane % LANES;
+    const bool on = r < t.tile_rows;
+    float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < parts; ++j) {
-      const float* src = first + (j ? j * STEP - RT * (D + 2) : 0);
-      const float f = ex2_approx(src[RT * D + r] - Mu);
-      const float4 x = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
-      L += f * src[RT * D + RT + r];
-      a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+    if (on) {
+#pragma unroll 4
+      for (int j = warp; j < t.parts; j += J_WARPS) {
+        const float* src = first + (j ? (2 * j - 1) * SIZE : 0);
+        const float m = src[RT * D + r], l = src[RT * D + RT + r];
+        const float4 x = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
+        const float nm = fmaxf(M, m), nu = nm == -INFINITY ? 0.f : nm;
+        const float f = ex2_approx(M - nu), h = ex2_approx(m - nu);
+        M = nm;
+        L = L * f + l * h;
+        a.x = a.x * f + x.x * h, a.y = a.y * f + x.y * h, a.z = a.z * f + x.z * h, a.w = a.w * f + x.w * h;
+      }
     }
-    const float inv = 1.f / L;
-    const int row = p.row0 + r, tok = row / k.group, h = p.head * k.group + row - tok * k.group;
-    *reinterpret_cast<uint2*>(k.out + (long)(p.e.a + tok) * k.ldo + h * D + 4 * d4) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    if (d4 == 0 && k.lse) k.lse[(long)(p.e.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+    s_a[warp][lane] = a;
+    s_m[warp][lane] = M;
+    s_l[warp][lane] = L;
+    __syncthreads();
+    if (warp == 0 && on) {
+      const int nw = min(t.parts, J_WARPS);
+      for (int w = 1; w < nw; ++w) M = fmaxf(M, s_m[w][lane]);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+      a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < nw; ++w) {
+        const float f = ex2_approx(s_m[w][lane] - Mu);
+        const float4 x = s_a[w][lane];
+        L += f * s_l[w][lane];
+        a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+      }
+      const float inv = 1.f / L;
+      const int row = t.row0 + r, tok = row / k.group, h = t.head * k.group + row - tok * k.group;
+      *reinterpret_cast<uint2*>(k.out + (long)(t.a + tok) * k.ldo + h * D + 4 * d4) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      if (d4 == 0 && k.lse) k.lse[(long)(t.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
@@ -612,32 +658,35 @@ static inline int ctas_per_sm(const Cache& c, int rt) { return rt * c.d <= 512 ?
 
 static inline size_t attention_workspace_bytes(const Cache& c, int H, int, int, int max_q) {
   const int rt = row_tile_of(c, H / c.kvh, max_q);
-  return (size_t)sm_count() * ctas_per_sm(c, rt) * 2 * rt * (c.d + 2) * 4;
+  return (size_t)sm_count() * ctas_per_sm(c, rt) * (sizeof(Join) + 2 * rt * (c.d + 2) * 4);
 }
 
 template <int FMT, int D, int NT>
-static inline cudaError_t stream_launch(const Call& k, cudaStream_t st) {
+static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t st) {
   constexpr int RT = 8 * NT;
-  const size_t pre = (size_t)(k.n + 1) * 8, smem = pre + (size_t)S_WARPS * RT * D * 4;
+  const size_t smem = Line::bytes(k.n) + (size_t)S_WARPS * RT * D * 4;
   static DeviceOnce once;
   cudaError_t e = run_once_per_device(once, [] {
     cudaError_t r = cudaFuncSetAttribute(stream_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (MAX_SEQS + 1) * 8 + S_WARPS * RT * D * 4);
+                                         (int)Line::bytes(MAX_SEQS) + S_WARPS * RT * D * 4);
     return r;
   });
   if (e != cudaSuccess) return e;
   const int grid = sm_count() * ctas_per_sm(k.c, RT);
-  stream_kernel<FMT, D, NT><<<grid, 32 * S_WARPS, smem, st>>>(k);
+  Call a = k;
+  a.join = static_cast<Join*>(work);
+  a.part = reinterpret_cast<float*>(a.join + grid);
+  stream_kernel<FMT, D, NT><<<grid, 32 * S_WARPS, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(join_kernel<D, RT>, dim3(grid), 128, pre, st, k);
+  return launch_after(join_kernel<D, RT>, dim3(grid), 32 * J_WARPS, 0, st, a);
 }
 template <int FMT>
-static inline cudaError_t stream_rows(const Call& k, cudaStream_t st) {
+static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st) {
   const int rt = row_tile_of(k.c, k.group, k.max_q);
   if (k.c.d == 64)
-    return rt == 8 ? stream_launch<FMT, 64, 1>(k, st) : rt == 16 ? stream_launch<FMT, 64, 2>(k, st) : stream_launch<FMT, 64, 4>(k, st);
-  return rt == 8 ? stream_launch<FMT, 128, 1>(k, st) : stream_launch<FMT, 128, 2>(k, st);
+    return rt == 8 ? stream_launch<FMT, 64, 1>(k, work, st) : rt == 16 ? stream_launch<FMT, 64, 2>(k, work, st) : stream_launch<FMT, 64, 4>(k, work, st);
+  return rt == 8 ? stream_launch<FMT, 128, 1>(k, work, st) : stream_launch<FMT, 128, 2>(k, work, st);
 }
 
 static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, long ldq, bf16* out, long ldo,
@@ -658,9 +707,11 @@ static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, lo
   k.lse = lse;
   k.slots = slots;
   k.cu = cu;
-  k.part = static_cast<float*>(work);
-  k.min_part = 2 * S_WARPS;
-  return c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, st) : stream_rows<GPT2_KV_E4M3>(k, st);
+  k.join = nullptr;
+  k.part = nullptr;
+  k.setup = c.d == 64 ? 8 : 4;
+  k.min_part = k.setup + 2 * S_WARPS;
+  return c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, work, st) : stream_rows<GPT2_KV_E4M3>(k, work, st);
 }
 
 }  // namespace kv8

@@ -242,10 +242,11 @@ CASES = [
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d,ps", [(64, 16), (128, 16), (64, 64), (128, 128)])
+@pytest.mark.parametrize("room", [256, 8192])  # tokens a slot may hold: tiles whole, or cut into parts
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_attention(fmt, d, ps, case):
+def test_attention(fmt, d, ps, case, room):
     lens, news, group, pad = CASES[case]
-    p = Pair(fmt, layers=2, kvh=1 if group > 4 else 3, d=d, ps=ps, num_pages=50, max_pages=256 // ps, seed=case)
+    p = Pair(fmt, layers=2, kvh=1 if group > 4 else 3, d=d, ps=ps, num_pages=50, max_pages=room // ps, seed=case)
     slots = [5, 0, 3, 7][:len(lens)]
     p.append([6], [19])               # so that the pages of the others are not 0, 1, ...
     p.append(slots, [max(0, t - n - 9) for t, n in zip(lens, news)])
@@ -268,10 +269,11 @@ def test_attention_long(fmt, d):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_attention_scales_far_apart(fmt):
+@pytest.mark.parametrize("room", [32, 256])
+def test_attention_scales_far_apart(fmt, room):
     """Pages whose values differ by many powers of two, scores far apart and
     far from zero, and queries with large and tiny components."""
-    p = Pair(fmt, kvh=2, ps=16, num_pages=60, max_pages=32)
+    p = Pair(fmt, kvh=2, ps=16, num_pages=60, max_pages=room)
     for i, size in enumerate([1e-6, 1.0, 300.0, 1e-3, 5.0]):
         p.append([0, 1], [33, 16], size=size)
     for size in (0.01, 1.0, 0.3):
@@ -309,9 +311,10 @@ def test_attention_nan_block_reaches_its_readers_only():
     assert torch.isnan(out[0, 0]).all() and not torch.isnan(out[0, 1]).any() and not torch.isnan(out[1]).any()
 
 
-def test_attention_refusals():
+@pytest.mark.parametrize("room", [16, 256])
+def test_attention_refusals(room):
     G = _g()
-    p = Pair(R.INT8)
+    p = Pair(R.INT8, max_pages=room)
     p.append([0, 1], [20, 50])
     q = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     out = torch.full_like(q, 7.0)

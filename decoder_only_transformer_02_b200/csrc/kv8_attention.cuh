@@ -107,6 +107,7 @@ struct Call {
   const int32_t *slots, *cu;
   Join* join;         // [grid]
   float* part;        // [grid][2][rows of a tile][d + 2]
+  int narrow;         // most rows per key/value head of a sequence that the streaming kernel takes
   int setup;          // units of the line that beginning a tile counts
   int min_part;       // fewest units of a CTA's part
 };
@@ -149,7 +150,7 @@ __device__ __forceinline__ bool lay_out(const Call& k, int row_tile, const Line&
         if (len < q || q > k.max_q) {
           q = 0;
           if (report) set_device_err(DERR_KV8_ARGS);
-        } else {
+        } else if ((long)q * k.group <= k.narrow) {
           x = (long long)k.c.kvh * row_tiles(k, q, row_tile) * (groups_of(len) + line.setup);
         }
       }
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
       if (threadIdx.x == 0) set_device_err(DERR_KV8_ARGS);
       return;
     }
+    if ((long)p.e.q * k.group > k.narrow) return;
   }
   const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_dyn) + warp * S::WARP;
@@ -336,6 +338,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         if (c.page_ok(pg)) {
           ksc = c.scales[c.unit(pg, k.layer, 0, p.head)];
           vsc = c.scales[c.unit(pg, k.layer, 1, p.head)];
+          if (!(vsc <= 3.0e38f)) ksc = vsc;  // a block that is not a number is none for the scores either
         } else {
           set_device_err(DERR_KV8_TABLE);
           pg = 0;
@@ -721,16 +724,21 @@ static inline int sm_count() {
   return n > 0 ? n : 148;
 }
 
+// Sequences with more rows per key/value head than this go to the tensor-core
+// kernel of kv8_prompt.cuh.
+constexpr int NARROW_ROWS = 64;
+static inline long narrow_rows(long rows) { return rows < NARROW_ROWS ? rows : NARROW_ROWS; }
+
 // rows of a tile: the call's rows per key/value head, 8 to 32 (16 at d = 128)
 static inline int row_tile_of(const Cache& c, int group, int max_q) {
-  const long r = (long)group * max_q;
+  const long r = narrow_rows((long)group * max_q);
   return r <= 8 ? 8 : r <= 16 || c.d == 128 ? 16 : 32;
 }
 static inline int parts_of(const Cache& c, int rt) {
   return sm_count() * ctas_of(rt, c.d);
 }
 
-static inline size_t attention_workspace_bytes(const Cache& c, int H, int, int, int max_q) {
+static inline size_t stream_workspace_bytes(const Cache& c, int H, int max_q) {
   const int rt = row_tile_of(c, H / c.kvh, max_q);
   return (size_t)parts_of(c, rt) * (sizeof(Join) + 2 * rt * (c.d + 2) * 4);
 }
@@ -747,7 +755,7 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
   if (e != cudaSuccess) return e;
   Call a = k;
   if (!SPLIT) {
-    const long tiles = (long)k.c.kvh * (((long)k.max_q * k.group + S::RT - 1) / S::RT);
+    const long tiles = (long)k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + S::RT - 1) / S::RT);
     stream_kernel<FMT, D, NT, W, SPLIT><<<dim3((unsigned)tiles, k.n), 32 * W, smem, st>>>(a);
     return cudaGetLastError();
   }
@@ -765,7 +773,7 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
 constexpr long WHOLE_TOKENS = 2048;
 template <int FMT, int D, int NT>
 static inline cudaError_t stream_mode(const Call& k, void* work, cudaStream_t st) {
-  const long tiles = (long)k.n * k.c.kvh * (((long)k.max_q * k.group + 8 * NT - 1) / (8 * NT));
+  const long tiles = (long)k.n * k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + 8 * NT - 1) / (8 * NT));
   if ((long)k.c.max_pages * k.c.ps <= WHOLE_TOKENS)
     return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false>(k, work, st) : stream_launch<FMT, D, NT, 4, false>(k, work, st);
   return stream_launch<FMT, D, NT, 4, true>(k, work, st);
@@ -778,29 +786,10 @@ static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st
   return rt == 8 ? stream_mode<FMT, 128, 1>(k, work, st) : stream_mode<FMT, 128, 2>(k, work, st);
 }
 
-static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, long ldq, bf16* out, long ldo,
-                                    float* lse, int H, const int32_t* slots, const int32_t* cu, int n, int rows,
-                                    int max_q, void* work, cudaStream_t st) {
-  Call k;
-  k.c = c;
-  k.layer = layer;
-  k.H = H;
-  k.group = H / c.kvh;
-  k.n = n;
-  k.rows = rows;
-  k.max_q = max_q;
-  k.q = q;
-  k.ldq = ldq;
-  k.out = out;
-  k.ldo = ldo;
-  k.lse = lse;
-  k.slots = slots;
-  k.cu = cu;
-  k.join = nullptr;
-  k.part = nullptr;
-  k.setup = c.d == 64 ? 16 : 4;
+static inline cudaError_t stream(Call k, void* work, cudaStream_t st) {
+  k.setup = k.c.d == 64 ? 16 : 4;
   k.min_part = k.setup + 8;
-  return c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, work, st) : stream_rows<GPT2_KV_E4M3>(k, work, st);
+  return k.c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, work, st) : stream_rows<GPT2_KV_E4M3>(k, work, st);
 }
 
 }  // namespace kv8

@@ -1,0 +1,714 @@
+// Attention of many new tokens per sequence over the paged 8-bit cache (the
+// chunks of a prompt), on the 5th-generation tensor cores.
+//
+// The rows of one sequence and key/value head, (token, head of the group)
+// pairs, are taken 256 at a time, as two tiles of 128 that share every key and
+// value block of 128 tokens:
+//   S_j = Q K_j^T     tcgen05.mma, M = 128, N = 128 keys, K = d, f16 in, fp32 in TMEM
+//   P_j = 2^(S_j f - m + 6) in f16, back into TMEM   (one thread per row)
+//   O  += P_j V_j     A = P_j from TMEM, N = d, K = 128 keys
+// and the result is O / sum P as in the streaming kernel (kv8_attention.cuh).
+//
+// The tensor cores read f16 from shared memory, the cache holds 8-bit codes, so
+// three warps convert each block on its way: the codes of the next 8 KB are
+// loaded while these 8 KB are converted and stored as swizzled f16 tiles.  A
+// key block's values are code * scale / (the block's largest scale), exact in
+// f16 unless 2^15 or more below it; the largest scale multiplies the scores.
+// Values are taken relative to the largest scale so far; when that rises, O is
+// scaled down as it is when the row maximum moves.
+//
+// Roles (384 threads, one CTA per SM; registers moved from the first four
+// warps to the softmax warps): warp 0 issues the MMAs of both tiles, warps 1-3
+// convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1.  Two tiles per
+// CTA instead of two CTAs of one tile: the conversion is done once for both,
+// and one tile's exponentials run while the other's MMAs do.
+//
+// As in the streaming kernel the key blocks of all tiles are one line of work
+// cut into equal parts, one per SM, and the cut tiles are joined by a second
+// kernel: 247 tiles of 300 to 1024 rows would load 148 SMs unevenly.
+//
+// All waits are bounded.
+#pragma once
+#include "attention_tc.cuh"
+#include "kv8_attention.cuh"
+
+namespace kv8 {
+
+constexpr int W_THREADS = 384;
+constexpr int W_ROWS = 256;  // rows of a work item (two tiles)
+constexpr int W_KEYS = 128;  // keys of a block
+
+template <int D>
+struct Wide {
+  static constexpr int NS = D == 64 ? 4 : 2;             // stages of the key/value ring
+  static constexpr int TILE = 128 * D * 2;               // one f16 tile: Q, K or V
+  static constexpr int KV_OFF = 2 * TILE;                // after the two Q tiles; stage s: K, V
+  static constexpr int BAR_OFF = KV_OFF + NS * 2 * TILE;
+  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale, value scale so far
+  static constexpr int LINE_OFF = INFO_OFF + 256;
+  static constexpr int UNIT_ROWS = 8192 / D;             // rows of an 8 KB unit of codes
+  static constexpr int UNITS = 2 * W_KEYS / UNIT_ROWS;   // of a block: keys, then values
+  // TMEM columns of a tile: S, P (in place of S's first 64 when d = 128), O
+  static constexpr uint32_t T_P = D == 64 ? 128 : 0, T_O = D == 64 ? 192 : 128;
+  static size_t bytes(int n) { return LINE_OFF + (size_t)(n + 1) * 8 + 1024; }
+};
+
+// f16 instruction descriptor: fp32 accumulate, M = 128; A K-major, B K-major or MN-major
+__host__ __device__ constexpr uint32_t f16_idesc(int n, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// V as B operand: rows of 128 bytes (64 dimensions), one per key; the second 64 dimensions 16 KB on
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------- the work line
+// Item j of a sequence (rows 256 j ..) and head takes the blocks up to its
+// last row's token, and `setup` units more.
+__device__ __forceinline__ int item_blocks(const Call& k, int len, int q, int j) {
+  const int last = min(q * k.group, (j + 1) * W_ROWS) - 1;
+  return (len - q + last / k.group) / W_KEYS + 1;
+}
+__device__ __forceinline__ int items_of(const Call& k, int q) { return (q * k.group + W_ROWS - 1) / W_ROWS; }
+
+__device__ __forceinline__ bool lay_out_wide(const Call& k, long long* pre, long long* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const bool report = blockIdx.x == 0;
+  long long base = 0;
+  bool bad = false;
+  for (int i0 = 0; i0 < k.n; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    long long x = 0;
+    if (i < k.n) {
+      const int a = k.cu[i], b = k.cu[i + 1], q = b - a;
+      bad |= a < 0 || b < a || b > k.rows;
+      if (q > 0 && (long)q * k.group > k.narrow) {
+        const int len = k.c.len_of(k.slots[i]);
+        if (len < q || q > k.max_q) {
+          if (report) set_device_err(DERR_KV8_ARGS);
+        } else if (b <= k.rows) {
+          const int items = items_of(k, q);
+          for (int j = 0; j < items; ++j) x += item_blocks(k, len, q, j) + k.setup;
+          x *= k.c.kvh;
+        }
+      }
+    }
+    const long long own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long before = base;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += s_warp[w];
+      base += s_warp[w];
+    }
+    if (i < k.n) pre[i] = before + x - own;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[k.n] = base;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0 && report) set_device_err(DERR_KV8_ARGS);
+    return false;
+  }
+  return true;
+}
+
+struct Item {
+  int slot, len, a, q, head, row0;  // row0: first of its rows
+  int b0, b1, blocks;               // blocks [b0, b1) of `blocks` are this part's
+  long long next;
+};
+__device__ __forceinline__ Item item_at(const Call& k, const long long* pre, long long at, long long end) {
+  int lo = 0, hi = k.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= at) lo = mid; else hi = mid;
+  }
+  Item p;
+  p.slot = k.slots[lo];
+  p.len = k.c.lens[p.slot];
+  p.a = k.cu[lo];
+  p.q = k.cu[lo + 1] - p.a;
+  long long rel = at - pre[lo];
+  int j = 0, size;
+  for (;; ++j) {  // head after head within an item's rows
+    p.blocks = item_blocks(k, p.len, p.q, j);
+    size = p.blocks + k.setup;
+    if (rel < (long long)size * k.c.kvh) break;
+    rel -= (long long)size * k.c.kvh;
+  }
+  p.head = (int)(rel / size);
+  p.row0 = j * W_ROWS;
+  const int u = (int)(rel - (long long)p.head * size);
+  p.next = min(at - u + size, end);
+  p.b0 = max(0, u - k.setup);
+  p.b1 = max(0, (int)(p.next - at) + u - k.setup);
+  return p;
+}
+
+// sixteen codes to f16 times a power of two (as a pair in f)
+template <int FMT>
+__device__ __forceinline__ void codes16_half(uint4 w, uint32_t f, uint32_t (&h)[8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  if (FMT == GPT2_KV_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * i]) : "r"(e4m3x2_to_half2(x[i] & 0xffffu)), "r"(f));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * i + 1]) : "r"(e4m3x2_to_half2(x[i] >> 16)), "r"(f));
+    }
+  } else {
+    uint32_t n;  // -1152 f
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n) : "r"(f), "r"(0xE480E480u));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = x[i] ^ 0x80808080u;  // code + 128, under the exponent of 1024
+      const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[2 * i]) : "r"(a), "r"(f), "r"(n));
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[2 * i + 1]) : "r"(b), "r"(f), "r"(n));
+    }
+  }
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
+  using S = Wide<D>;
+  using namespace tcg;
+  using namespace tcfa;
+  constexpr int NS = S::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);  // NS, count 3 (converting warps)
+  uint64_t* kv_empty = kv_full + NS;                                   // NS: both tiles' MMAs have read the stage
+  uint64_t* q_full = kv_empty + NS;                                    // 2, count 4: the tile's Q is in shared memory
+  uint64_t* s_full = q_full + 2;                                       // 2: S in TMEM
+  uint64_t* s_free = s_full + 2;                                       // 2, count 4: S is in registers
+  uint64_t* p_full = s_free + 2;                                       // 2, count 4: P in TMEM (and O rescaled)
+  uint64_t* pv_done = p_full + 2;                                      // 2: O += P V complete
+  uint64_t* drain = pv_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  float2* info = reinterpret_cast<float2*>(smem + S::INFO_OFF);
+  long long* s_warp = reinterpret_cast<long long*>(smem + S::INFO_OFF + 128);
+  long long* pre = reinterpret_cast<long long*>(smem + S::LINE_OFF);
+  const Cache& c = k.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kv_full[s], 3);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&q_full[a], 4);
+      mbar_init(&s_full[a], 1);
+      mbar_init(&s_free[a], 4);
+      mbar_init(&p_full[a], 4);
+      mbar_init(&pv_done[a], 1);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const bool line_ok = lay_out_wide(k, pre, s_warp);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long total = line_ok ? pre[k.n] : 0;
+  const long long per = max((long long)k.min_part, (total + gridDim.x - 1) / gridDim.x);
+  long long at = blockIdx.x * per;
+  const long long end = min(total, at + per);
+
+  if (warp < 4) {
+    regs_down<104>();
+    if (warp == 0) {
+      if (lane == 0) {
+        // ---------------------------------------------------- MMA issuer
+        constexpr uint32_t id_s = f16_idesc(W_KEYS, 0), id_pv = f16_idesc(D, 1);
+        uint32_t g = 0, t[2] = {0, 0}, items[2] = {0, 0};
+        bool ok = true;
+        int join_parts = 0;
+        auto do_s = [&](int a, int stage) {
+          const uint32_t qa = smem_u32(smem + a * S::TILE), ka = smem_u32(smem + S::KV_OFF + 2 * stage * S::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+            tc_mma(tmem + a * 256, make_sdesc(qa + o, 0), make_sdesc(ka + o, 0), id_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[a]);
+        };
+        auto do_pv = [&](int a, int stage, bool first) -> bool {  // of the tile's latest S
+          if (!mbar_wait(&p_full[a], (t[a] - 1) & 1u)) return false;
+          tc_fence_after();
+          const uint32_t va = smem_u32(smem + S::KV_OFF + (2 * stage + 1) * S::TILE);
+#pragma unroll
+          for (int kk = 0; kk < W_KEYS / 16; ++kk)
+            tc_mma_ts(tmem + a * 256 + S::T_O, tmem + a * 256 + S::T_P + kk * 8, v_desc(va + kk * 2048), id_pv,
+                      first && kk == 0 ? 0u : 1u);
+          tc_commit(&pv_done[a]);
+          return true;
+        };
+        while (ok && at < end) {
+          const Item p = item_at(k, pre, at, end);
+          const int rows = p.q * k.group - p.row0;
+          if (p.b0 == 0 && p.b1 > 0 && p.b1 < p.blocks) {
+            join_parts = (int)((p.next + p.blocks - p.b1 - 1) / per) - blockIdx.x + 1;
+            Join j;
+            j.parts = join_parts, j.tile_rows = min(W_ROWS, rows), j.row0 = p.row0, j.head = p.head, j.a = p.a;
+            k.join[blockIdx.x] = j;
+          }
+          at = p.next;
+          const int tiles = rows > 128 ? 2 : 1;
+          for (int j = p.b0; ok && j < p.b1; ++j, ++g) {
+            const int s = g % NS, sp = (g + NS - 1) % NS;
+            if (!mbar_wait(&kv_full[s], (g / NS) & 1u)) {
+              ok = false;
+              break;
+            }
+            for (int a = 0; a < tiles; ++a) {
+              if (j == p.b0) {
+                if (!mbar_wait(&q_full[a], items[a] & 1u)) {
+                  ok = false;
+                  break;
+                }
+                ++items[a];
+              } else if (D == 64) {
+                if (!mbar_wait(&s_free[a], (t[a] - 1) & 1u)) {
+                  ok = false;
+                  break;
+                }
+              } else if (!do_pv(a, sp, j - 1 == p.b0)) {  // P lies in S's place: its product goes first
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              do_s(a, s);
+              if (D == 64 && j > p.b0 && !do_pv(a, sp, j - 1 == p.b0)) {
+                ok = false;
+                break;
+              }
+              ++t[a];
+            }
+            if (ok && j > p.b0) tc_commit(&kv_empty[sp]);
+          }
+          if (ok && p.b1 > p.b0) {
+            const int sp = (g + NS - 1) % NS;
+            for (int a = 0; ok && a < tiles; ++a) ok = do_pv(a, sp, p.b1 - 1 == p.b0);
+            if (ok) tc_commit(&kv_empty[sp]);
+          }
+        }
+        if (join_parts == 0) k.join[blockIdx.x].parts = 0;
+        if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
+        tc_commit(drain);
+        if (!mbar_wait_drain(drain, 0)) set_device_err(DERR_WAIT_TIMEOUT);
+      }
+    } else {
+      // ------------------------------------------------ converting warps
+      constexpr int PER_ROW = D / 16, LOADS = (512 + 95) / 96;
+      const int pt = threadIdx.x - 32;
+      uint32_t g = 0;
+      bool ok = true;
+      const long page_stride = c.page_bytes();
+      const long side_stride = (long)c.kvh * c.ps * D;
+      while (ok && at < end) {
+        const Item p = item_at(k, pre, at, end);
+        at = p.next;
+        if (p.b1 == p.b0) continue;
+        const int32_t* table = c.table + (long)p.slot * c.max_pages;
+        const uint8_t* head_base = c.codes + ((long)k.layer * 2 * c.kvh + p.head) * c.ps * D;
+        const int per_block = W_KEYS >> c.ps_log2;  // pages of a block
+        // lane x: page x of a block, and its scales (0: behind the last token)
+        struct Pages {
+          int pg;
+          float ks, vs;
+        };
+        auto pages = [&](int blk) {
+          Pages x = {0, 0.f, 0.f};
+          const int tok = blk * W_KEYS + (lane << c.ps_log2);
+          if (lane < per_block && tok < p.len) {
+            x.pg = table[tok >> c.ps_log2];
+            if (c.page_ok(x.pg)) {
+              x.ks = c.scales[c.unit(x.pg, k.layer, 0, p.head)];
+              x.vs = c.scales[c.unit(x.pg, k.layer, 1, p.head)];
+            } else {
+              set_device_err(DERR_KV8_TABLE);
+              x.pg = 0;
+              x.ks = x.vs = __uint_as_float(NAN_SCALE);
+            }
+          }
+          return x;
+        };
+        uint4 nx[LOADS];
+        auto load = [&](int pg, int blk, int unit) {  // 8 KB of codes: this thread's pieces; zeros behind the last token
+          const int side = unit >= S::UNITS / 2, part = unit - side * (S::UNITS / 2);
+          const uint8_t* src = head_base + side * side_stride;
+#pragma unroll
+          for (int e = 0; e < LOADS; ++e) {
+            const int i = pt + 96 * e, row = min(i / PER_ROW, S::UNIT_ROWS - 1) + part * S::UNIT_ROWS;
+            const int page = __shfl_sync(0xffffffffu, pg, row >> c.ps_log2);
+            nx[e] = make_uint4(0, 0, 0, 0);
+            if (i < 512 && blk * W_KEYS + row < p.len)
+              nx[e] = __ldcg(reinterpret_cast<const uint4*>(src + page * page_stride + ((row & (c.ps - 1)) * D + (i % PER_ROW) * 16)));
+          }
+        };
+        float vref = 0.f;
+        Pages now = pages(p.b0);
+        load(now.pg, p.b0, 0);
+        for (int j = p.b0; j < p.b1; ++j, ++g) {
+          const int s = g % NS;
+          Pages next = {0, 0.f, 0.f};
+          if (j + 1 < p.b1) next = pages(j + 1);
+          // factors of the block's pages
+          const bool nan = !(now.ks <= 3.0e38f && now.vs <= 3.0e38f);
+          const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(now.ks)))));
+          const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(now.vs)))));
+          vref = fmaxf(vref, vmax);
+          const float kr = now.ks * (1.f / kmax), vr = now.vs * (1.f / vref);
+          // a page with a scale that is not a number: its keys are not, its values 0 (only rows that see it notice)
+          const uint32_t kf = nan ? 0x7e007e00u : half2_of(kr, kr), vf = nan ? 0u : half2_of(vr, vr);
+          if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((g / NS) & 1u) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          if (pt == 0) info[s] = make_float2(kmax, vref);
+#pragma unroll
+          for (int u = 0; u < S::UNITS; ++u) {
+            uint4 cur[LOADS];
+#pragma unroll
+            for (int e = 0; e < LOADS; ++e) cur[e] = nx[e];
+            if (u + 1 < S::UNITS) load(now.pg, j, u + 1);
+            else if (j + 1 < p.b1) load(next.pg, j + 1, 0);
+            const int side = u >= S::UNITS / 2, part = u - side * (S::UNITS / 2);
+            const uint32_t dst = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE);
+#pragma unroll
+            for (int e = 0; e < LOADS; ++e) {
+              const int i = pt + 96 * e, row = min(i / PER_ROW, S::UNIT_ROWS - 1) + part * S::UNIT_ROWS, q = i % PER_ROW;
+              const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row >> c.ps_log2);
+              uint32_t h[8];
+              codes16_half<FMT>(cur[e], f, h);
+              if (i < 512) {
+                // the two 16-byte pieces in an order that keeps eight lanes in different banks
+                const bool x = D == 128 && ((q >> 2) & 1);
+                const uint32_t tile = dst + (D == 128 ? (q >> 2) * 16384 : 0);
+                const uint32_t a0 = tile + sw128(row, (2 * q) & 7), a1 = tile + sw128(row, (2 * q + 1) & 7);
+                sts128(x ? a1 : a0, x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2], x ? h[7] : h[3]);
+                sts128(x ? a0 : a1, x ? h[0] : h[4], x ? h[1] : h[5], x ? h[2] : h[6], x ? h[3] : h[7]);
+              }
+            }
+          }
+          now = next;
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[s]);
+        }
+      }
+      if (!ok && lane == 0) set_device_err(DERR_WAIT_TIMEOUT);
+    }
+  } else {
+    // -------------------------------------------------- softmax of a tile
+    regs_up<200>();
+    const int a = (warp >> 2) - 1, qw = warp & 3, r = qw * 32 + lane;
+    const uint32_t tl = tmem + a * 256 + ((uint32_t)(qw * 32) << 16);
+    const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
+    uint32_t g = 0, t = 0;
+    bool ok = true;
+    while (ok && at < end) {
+      const Item p = item_at(k, pre, at, end);
+      at = p.next;
+      const int rows = p.q * k.group - p.row0 - a * 128;  // of this tile and those after it
+      if (rows <= 0) {
+        g += p.b1 - p.b0;
+        continue;
+      }
+      if (p.b1 == p.b0) continue;
+      const bool on = r < rows;
+      const int row = p.row0 + a * 128 + (on ? r : 0), tok = row / k.group, h = p.head * k.group + row - tok * k.group;
+      const int pos = p.len - p.q + tok;  // the last token the row sees
+      // the tile's first row sees the fewest
+      const int first_pos = p.len - p.q + (p.row0 + a * 128) / k.group;
+      // ---- Q: the row times a power of two, as f16
+      float rowf;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(k.q + (long)(p.a + tok) * k.ldq + h * D);
+        uint4 x[D / 8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          x[e] = on ? src[e] : make_uint4(0, 0, 0, 0);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                                     __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu)));
+        }
+        const int E = max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15);
+        const float up = __uint_as_float((uint32_t)(268 - E) << 23);
+        rowf = __uint_as_float((uint32_t)(E - 14) << 23) * sl2;
+        const uint32_t dst = smem_u32(smem + a * S::TILE);
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_bf16x2(w[i]);
+            y[i] = half2_of(f.x * up, f.y * up);
+          }
+          sts128(dst + (e >> 3) * 16384 + sw128(r, e & 7), y[0], y[1], y[2], y[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[a]);
+      }
+      float m = -INFINITY, l = 0.f, vref = 0.f;
+      for (int j = p.b0; j < p.b1; ++j, ++g, ++t) {
+        if (!warp_wait(&s_full[a], t & 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const volatile float2* at_info = &info[g % NS];
+        const float2 scale = make_float2(at_info->x, at_info->y);
+        const float fs = fmaxf(scale.x * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
+        uint32_t v[W_KEYS];
+        tmem_ld64(tl, v);
+        tmem_ld64(tl + 64, v + 64);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (D == 64 && lane == 0) mbar_arrive(&s_free[a]);
+        if (j * W_KEYS + W_KEYS - 1 > first_pos) {
+#pragma unroll
+          for (int e = 0; e < W_KEYS; ++e)
+            if (j * W_KEYS + e > pos) v[e] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[i]);
+#pragma unroll
+        for (int e = 8; e < W_KEYS; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(v[e]));
+        const float mx = fs * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                    fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        // the reference moves when a row passes it by 2^8, and O also when the value scale rises
+        const bool moved = __any_sync(0xffffffffu, mx > m + 8.f);
+        const bool rescale = moved || scale.y > vref;
+        float alpha = 1.f;
+        if (moved) {
+          const float nm = fmaxf(m, mx);
+          alpha = m == -INFINITY ? 0.f : ex2f(m - nm);
+          m = nm;
+          l *= alpha;
+        }
+        if (scale.y > vref) {
+          alpha *= vref / scale.y;
+          vref = scale.y;
+        }
+        const float off = m == -INFINITY ? 0.f : m - 6.f;  // weights up to 2^14 in f16, down to 2^-30 of the reference
+        float rs8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rs8[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < W_KEYS; e += 2) {
+          const float p0 = ex2f(fmaf(__uint_as_float(v[e]), fs, -off));
+          const float p1 = ex2f(fmaf(__uint_as_float(v[e + 1]), fs, -off));
+          rs8[e & 7] += p0;
+          rs8[(e + 1) & 7] += p1;
+          v[e >> 1] = half2_of(p0, p1);
+        }
+        l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+        if (j > p.b0) {
+          if (!warp_wait(&pv_done[a], (t - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (rescale) {
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tl + S::T_O + q * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tl + S::T_O + q * 32, o);
+            }
+          }
+        }
+        tmem_st32(tl + S::T_P, v);
+        tmem_st32(tl + S::T_P + 32, v + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[a]);
+      }
+      if (!ok || !warp_wait(&pv_done[a], (t - 1) & 1u)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // ---- the item's result, or this part's share of it
+      const bool whole = p.b0 == 0 && p.b1 == p.blocks;
+      float* part = k.part + ((long)blockIdx.x * 2 + (p.b0 == 0)) * W_ROWS * (D + 2);
+      const int pr = a * 128 + r;
+      const float M = m - 6.f;  // the sums' reference
+      const float f = whole ? vref / l : vref;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tl + S::T_O + q * 32, o);
+        tmem_wait_ld();
+        if (on && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(k.out + (long)(p.a + tok) * k.ldo + h * D + q * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f),
+                                pack_bf16x2(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f),
+                                pack_bf16x2(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f),
+                                pack_bf16x2(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f));
+        } else if (on) {
+          float4* dst = reinterpret_cast<float4*>(part + pr * D + q * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                 __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+        }
+      }
+      tc_fence_before();
+      if (on && !whole) {
+        part[W_ROWS * D + pr] = M;
+        part[W_ROWS * D + W_ROWS + pr] = l;
+      }
+      if (on && whole && k.lse) k.lse[(long)(p.a + tok) * k.H + h] = (M + log2f(l)) * 0.6931471805599453f;
+    }
+    if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// CTA (x, y): rows 32 y .. of the item that begins in part x and goes on after it.
+template <int D>
+__global__ void __launch_bounds__(256) join_wide_kernel(const Call k) {
+  pdl_wait();
+  const Join t = k.join[blockIdx.x];
+  if (t.parts == 0) return;
+  constexpr long SIZE = (long)W_ROWS * (D + 2);
+  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
+  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
+    const int r = blockIdx.y * 32 + i / (D / 4), d4 = i % (D / 4);
+    if (r >= t.tile_rows) break;
+    float M = -INFINITY, L = 0.f;
+    for (int j = 0; j < t.parts; ++j) M = fmaxf(M, first[(j ? (2 * j - 1) * SIZE : 0) + W_ROWS * D + r]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int j = 0; j < t.parts; ++j) {
+      const float* src = first + (j ? (2 * j - 1) * SIZE : 0);
+      const float f = ex2_approx(src[W_ROWS * D + r] - Mu);
+      const float4 x = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
+      L += f * src[W_ROWS * D + W_ROWS + r];
+      a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+    }
+    const float inv = 1.f / L;
+    const int row = t.row0 + r, tok = row / k.group, h = t.head * k.group + row - tok * k.group;
+    *reinterpret_cast<uint2*>(k.out + (long)(t.a + tok) * k.ldo + h * D + 4 * d4) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (d4 == 0 && k.lse) k.lse[(long)(t.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+static inline size_t wide_workspace_bytes(const Cache& c) {
+  return (size_t)sm_count() * (sizeof(Join) + 2 * (size_t)W_ROWS * (c.d + 2) * 4);
+}
+
+template <int FMT, int D>
+static inline cudaError_t wide_launch(const Call& k, void* work, cudaStream_t st) {
+  using S = Wide<D>;
+  static DeviceOnce once;
+  cudaError_t e = run_once_per_device(once, [] {
+    return cudaFuncSetAttribute(wide_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes(MAX_SEQS));
+  });
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count();
+  Call a = k;
+  a.join = static_cast<Join*>(work);
+  a.part = reinterpret_cast<float*>(a.join + grid);
+  a.setup = 2;
+  a.min_part = 4;
+  wide_kernel<FMT, D><<<grid, W_THREADS, S::bytes(k.n), st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(join_wide_kernel<D>, dim3(grid, W_ROWS / 32), 256, 0, st, a);
+}
+
+static inline cudaError_t wide(const Call& k, void* work, cudaStream_t st) {
+  if (k.c.fmt == GPT2_KV_INT8)
+    return k.c.d == 64 ? wide_launch<GPT2_KV_INT8, 64>(k, work, st) : wide_launch<GPT2_KV_INT8, 128>(k, work, st);
+  return k.c.d == 64 ? wide_launch<GPT2_KV_E4M3, 64>(k, work, st) : wide_launch<GPT2_KV_E4M3, 128>(k, work, st);
+}
+
+// ---------------------------------------------------------------- the call
+// One sequence: whichever kernel suits max_q takes it, whatever its rows.
+// More: each sequence goes by its own rows, so that single tokens and prompts
+// may share a call; without a prompt (max_q) the wide kernel is not launched.
+static inline int narrow_limit(int group, int n, int max_q) {
+  return (long)group * max_q <= NARROW_ROWS ? NARROW_ROWS : n == 1 ? 0 : NARROW_ROWS;
+}
+
+static inline size_t attention_workspace_bytes(const Cache& c, int H, int n, int, int max_q) {
+  const int group = H / c.kvh;
+  const size_t a = narrow_limit(group, n, max_q) ? stream_workspace_bytes(c, H, max_q) : 0;
+  const size_t b = (long)group * max_q > NARROW_ROWS ? wide_workspace_bytes(c) : 0;
+  return a > b ? a : b;  // the kernels run one after the other
+}
+
+static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, long ldq, bf16* out, long ldo,
+                                    float* lse, int H, const int32_t* slots, const int32_t* cu, int n, int rows,
+                                    int max_q, void* work, cudaStream_t st) {
+  Call k;
+  k.c = c;
+  k.layer = layer;
+  k.H = H;
+  k.group = H / c.kvh;
+  k.n = n;
+  k.rows = rows;
+  k.max_q = max_q < rows ? max_q : rows;
+  k.q = q;
+  k.ldq = ldq;
+  k.out = out;
+  k.ldo = ldo;
+  k.lse = lse;
+  k.slots = slots;
+  k.cu = cu;
+  k.join = nullptr;
+  k.part = nullptr;
+  k.narrow = narrow_limit(k.group, n, max_q);
+  k.setup = k.min_part = 0;
+  if (k.narrow) {
+    const cudaError_t e = stream(k, work, st);
+    if (e != cudaSuccess) return e;
+  }
+  return (long)k.group * max_q > NARROW_ROWS ? wide(k, work, st) : cudaSuccess;
+}
+
+}  // namespace kv8

@@ -4,7 +4,7 @@
 #include "tc_gemm.cu"
 #include "attention_tc.cuh"
 #include "attention_tc_bwd.cuh"
-#include "kv8_attention.cuh"
+#include "kv8_prompt.cuh"
 #include "model_pass.cuh"
 #include "model_decode.cuh"
 

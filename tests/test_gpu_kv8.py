@@ -256,6 +256,32 @@ def test_attention(fmt, d, ps, case, room):
         p.attention(slots, news, group, pad, layer=layer)
 
 
+PROMPTS = [
+    # lens, new rows, group: more than 64 rows per key/value head
+    ([65], [65], 1),
+    ([128, 129, 300], [128, 129, 300], 1),
+    ([700, 1, 40, 513], [257, 1, 40, 130], 1),   # prompts, a single token and a few tokens in one call
+    ([1000, 90], [33, 3], 8),                    # rows of one token in two tiles
+    ([500, 300], [100, 299], 3),
+    ([70], [2], 40),
+    ([1100], [600], 1),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 32), (64, 128), (128, 128)])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_attention_of_prompts(fmt, d, ps, case):
+    lens, news, group = PROMPTS[case]
+    p = Pair(fmt, layers=2, kvh=2, d=d, ps=ps, num_pages=150, max_pages=1200 // ps + 1, seed=100 + case)
+    slots = [5, 0, 3, 7][:len(lens)]
+    p.append([6], [19])
+    p.append(slots, [t // 2 for t in lens], size=2.0)
+    p.append(slots[::-1], [t - t // 2 for t in lens][::-1], size=0.7)
+    p.attention(slots, news, group, pad=2, layer=1)
+    p.attention(slots, news, group, layer=0, max_q=1200)  # max_q may be more than any sequence has
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_long(fmt, d):
@@ -266,6 +292,7 @@ def test_attention_long(fmt, d):
     p.attention([1, 2, 4], [1, 1, 1], group=2)
     p.attention([2, 4], [5, 1], group=1, pad=1)
     p.attention([2], [40], group=2, size=2.0)
+    p.attention([2, 1], [70, 300], group=1)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -282,6 +309,8 @@ def test_attention_scales_far_apart(fmt, room):
         p.append([2], [40], size=1e-20)
     p.attention([2], [3], size=1e15)
     p.attention([2], [3], size=1e-15)
+    for size in (0.01, 1.0):
+        p.attention([0, 1], [70, 66], group=1, size=size)
 
 
 def test_attention_equal_scores_and_zero_values():
@@ -290,8 +319,9 @@ def test_attention_equal_scores_and_zero_values():
     def zero(x):
         x[:] = 0
     p.append([0], [70], mutate=zero)
-    out, lse = p.attention([0], [2])
-    assert torch.all(out == 0)
+    for rows in (2, 70):
+        out, lse = p.attention([0], [rows])
+        assert torch.all(out == 0)
 
 
 def test_attention_nan_block_reaches_its_readers_only():
@@ -309,6 +339,21 @@ def test_attention_nan_block_reaches_its_readers_only():
     p.dev.attention(0, q, out, _i32([0, 1]), _i32([0, 1, 2]), 1, work)
     p.G.check_device_error()
     assert torch.isnan(out[0, 0]).all() and not torch.isnan(out[0, 1]).any() and not torch.isnan(out[1]).any()
+    # in values too, and with many rows: those before the block do not see it
+    p.append([2], [100])
+
+    def bad_value(x):
+        x[0, 128:192] = np.inf  # values of head 0
+    p.append([2], [20], mutate=bad_value)  # positions 100 .. 119, in the pages from 96
+    for rows in (40, 90):
+        out = torch.zeros(rows, 2, 64, dtype=torch.bfloat16, device="cuda")
+        q = torch.ones_like(out)
+        work = torch.empty(p.dev.attention_workspace_bytes(2, 1, rows, rows), dtype=torch.uint8, device="cuda")
+        p.dev.attention(0, q, out, _i32([2]), _i32([0, rows]), rows, work)
+        p.G.check_device_error()
+        sees = torch.arange(120 - rows, 120, device="cuda") >= 96
+        assert torch.equal(torch.isnan(out[:, 0]).all(-1), sees) and torch.equal(torch.isnan(out[:, 0]).any(-1), sees)
+        assert not torch.isnan(out[:, 1]).any()
 
 
 @pytest.mark.parametrize("room", [16, 256])

@@ -110,6 +110,7 @@ struct Call {
   int narrow;         // most rows per key/value head of a sequence that the streaming kernel takes
   int setup;          // units of the line that beginning a tile counts
   int min_part;       // fewest units of a CTA's part
+  uint32_t zero;      // 0
 };
 
 struct Entry {
@@ -288,14 +289,15 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
     p.next = 1;
     if (__syncthreads_or(bad)) {
       if (threadIdx.x == 0) set_device_err(DERR_KV8_ARGS);
-      return;
-    }
-    if (p.e.q <= 0 || (long)p.row0 >= (long)p.e.q * k.group) return;
-    if (p.e.len < p.e.q || p.e.q > k.max_q) {
+      at = end;
+    } else if (p.e.q <= 0 || (long)p.row0 >= (long)p.e.q * k.group) {
+      at = end;
+    } else if (p.e.len < p.e.q || p.e.q > k.max_q) {
       if (threadIdx.x == 0) set_device_err(DERR_KV8_ARGS);
-      return;
+      at = end;
+    } else if ((long)p.e.q * k.group > k.narrow) {
+      at = end;
     }
-    if ((long)p.e.q * k.group > k.narrow) return;
   }
   const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_dyn) + warp * S::WARP;
@@ -654,6 +656,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
     __syncthreads();
   }
   if (SPLIT && join_parts == 0 && threadIdx.x == 0) k.join[blockIdx.x].parts = 0;
+  pdl_wait();  // (behind the wide kernel: this one does not end before it)
 }
 
 // CTA x joins the tile that began in part x of the line and went on past it:
@@ -744,7 +747,7 @@ static inline size_t stream_workspace_bytes(const Cache& c, int H, int max_q) {
 }
 
 template <int FMT, int D, int NT, int W, bool SPLIT>
-static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t st) {
+static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t st, bool behind) {
   using S = Shape<D, NT, W>;
   const size_t smem = S::BYTES + (SPLIT ? Line::bytes(k.n) : 0);
   static DeviceOnce once;
@@ -756,14 +759,20 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
   Call a = k;
   if (!SPLIT) {
     const long tiles = (long)k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + S::RT - 1) / S::RT);
-    stream_kernel<FMT, D, NT, W, SPLIT><<<dim3((unsigned)tiles, k.n), 32 * W, smem, st>>>(a);
+    const dim3 grid((unsigned)tiles, k.n);
+    if (behind) return launch_after(stream_kernel<FMT, D, NT, W, SPLIT>, grid, 32 * W, smem, st, a);
+    stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
     return cudaGetLastError();
   }
   const int grid = parts_of(k.c, S::RT);
   a.join = static_cast<Join*>(work);
   a.part = reinterpret_cast<float*>(a.join + grid);
-  stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
-  e = cudaGetLastError();
+  if (behind) {
+    e = launch_after(stream_kernel<FMT, D, NT, W, SPLIT>, dim3(grid), 32 * W, smem, st, a);
+  } else {
+    stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_after(join_kernel<D, S::RT>, dim3(grid), 32 * J_WARPS, 0, st, a);
 }
@@ -772,24 +781,25 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
 // one sequence of 777: 6.3 (eight warps; sixteen 7.2), and cut 8.9.
 constexpr long WHOLE_TOKENS = 2048;
 template <int FMT, int D, int NT>
-static inline cudaError_t stream_mode(const Call& k, void* work, cudaStream_t st) {
+static inline cudaError_t stream_mode(const Call& k, void* work, cudaStream_t st, bool behind) {
   const long tiles = (long)k.n * k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + 8 * NT - 1) / (8 * NT));
   if ((long)k.c.max_pages * k.c.ps <= WHOLE_TOKENS)
-    return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false>(k, work, st) : stream_launch<FMT, D, NT, 4, false>(k, work, st);
-  return stream_launch<FMT, D, NT, 4, true>(k, work, st);
+    return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false>(k, work, st, behind) : stream_launch<FMT, D, NT, 4, false>(k, work, st, behind);
+  return stream_launch<FMT, D, NT, 4, true>(k, work, st, behind);
 }
 template <int FMT>
-static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st) {
+static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st, bool behind) {
   const int rt = row_tile_of(k.c, k.group, k.max_q);
   if (k.c.d == 64)
-    return rt == 8 ? stream_mode<FMT, 64, 1>(k, work, st) : rt == 16 ? stream_mode<FMT, 64, 2>(k, work, st) : stream_mode<FMT, 64, 4>(k, work, st);
-  return rt == 8 ? stream_mode<FMT, 128, 1>(k, work, st) : stream_mode<FMT, 128, 2>(k, work, st);
+    return rt == 8 ? stream_mode<FMT, 64, 1>(k, work, st, behind) : rt == 16 ? stream_mode<FMT, 64, 2>(k, work, st, behind) : stream_mode<FMT, 64, 4>(k, work, st, behind);
+  return rt == 8 ? stream_mode<FMT, 128, 1>(k, work, st, behind) : stream_mode<FMT, 128, 2>(k, work, st, behind);
 }
 
-static inline cudaError_t stream(Call k, void* work, cudaStream_t st) {
+// behind: it follows the wide kernel of the same call and may start before that one ends
+static inline cudaError_t stream(Call k, void* work, cudaStream_t st, bool behind) {
   k.setup = k.c.d == 64 ? 16 : 4;
   k.min_part = k.setup + 8;
-  return k.c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, work, st) : stream_rows<GPT2_KV_E4M3>(k, work, st);
+  return k.c.fmt == GPT2_KV_INT8 ? stream_rows<GPT2_KV_INT8>(k, work, st, behind) : stream_rows<GPT2_KV_E4M3>(k, work, st, behind);
 }
 
 }  // namespace kv8

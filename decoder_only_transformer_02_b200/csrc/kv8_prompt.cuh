@@ -10,15 +10,14 @@
 // and the result is O / sum P as in the streaming kernel (kv8_attention.cuh).
 //
 // The tensor cores read f16 from shared memory, the cache holds 8-bit codes, so
-// three warps convert each block on its way: the codes of the next 8 KB are
-// loaded while these 8 KB are converted and stored as swizzled f16 tiles.  A
+// seven warps convert each block on its way: the codes of the next 16 KB are
+// loaded while these 16 KB are converted and stored as swizzled f16 tiles.  A
 // key block's values are code * scale / (the block's largest scale), exact in
 // f16 unless 2^15 or more below it; the largest scale multiplies the scores.
 // Values are taken relative to the largest scale so far; when that rises, O is
 // scaled down as it is when the row maximum moves.
 //
-// Roles (384 threads, one CTA per SM; registers moved from the first four
-// warps to the softmax warps): warp 0 issues the MMAs of both tiles, warps 1-3
+// Roles (512 threads, one CTA per SM, some registers moved to the softmax): warp 0 issues the MMAs of both tiles, warps 1-3 and 12-15
 // convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1.  Two tiles per
 // CTA instead of two CTAs of one tile: the conversion is done once for both,
 // and one tile's exponentials run while the other's MMAs do.
@@ -34,7 +33,11 @@
 
 namespace kv8 {
 
-constexpr int W_THREADS = 384;
+constexpr int W_THREADS = 512;
+constexpr int W_CONV = 7;    // converting warps
+// registers of a thread: 8 softmax warps and 8 others share the 16 * 32 * 128 of the launch
+constexpr int W_REGS_LOW = 112, W_REGS_HIGH = 144;
+static_assert(W_REGS_LOW + W_REGS_HIGH == 2 * 128, "the launch's registers, no more");
 constexpr int W_ROWS = 256;  // rows of a work item (two tiles)
 constexpr int W_KEYS = 128;  // keys of a block
 
@@ -44,15 +47,41 @@ struct Wide {
   static constexpr int TILE = 128 * D * 2;               // one f16 tile: Q, K or V
   static constexpr int KV_OFF = 2 * TILE;                // after the two Q tiles; stage s: K, V
   static constexpr int BAR_OFF = KV_OFF + NS * 2 * TILE;
-  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale, value scale so far
+  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale (negative: some page's is not a number), value scale so far
   static constexpr int LINE_OFF = INFO_OFF + 256;
-  static constexpr int UNIT_ROWS = 8192 / D;             // rows of an 8 KB unit of codes
-  static constexpr int UNITS = 2 * W_KEYS / UNIT_ROWS;   // of a block: keys, then values
+  static constexpr int UNITS = D / 64;                   // 16 KB units of codes in a block: all of it, or keys, values
   // TMEM columns of a tile: S, P (in place of S's first 64 when d = 128), O
   static constexpr uint32_t T_P = D == 64 ? 128 : 0, T_O = D == 64 ? 192 : 128;
   static size_t bytes(int n) { return LINE_OFF + (size_t)(n + 1) * 8 + 1024; }
 };
 
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 2^x of two values on the FMA and integer pipes (MUFU's 16 a cycle are what
+// the softmax waits for): n = x to the nearest integer by adding 1.5 * 2^23,
+// 2^(x - n) from a polynomial of degree 4 fitted here to the least largest
+// relative error on [-1/2, 1/2] (2.7e-6), n added to the exponent.  x from -126 to 126.
+__device__ __forceinline__ float2 ex2_fma2(float2 x) {
+  const float2 big = make_float2(12582912.f, 12582912.f);
+  const float2 t = add2(x, big), f = sub2(x, sub2(t, big));
+  float2 y = fma2(make_float2(0.009570102207362652f, 0.009570102207362652f), f, make_float2(0.05591786280274391f, 0.05591786280274391f));
+  y = fma2(y, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  y = fma2(y, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  y = fma2(y, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
 // f16 instruction descriptor: fp32 accumulate, M = 128; A K-major, B K-major or MN-major
 __host__ __device__ constexpr uint32_t f16_idesc(int n, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -62,15 +91,6 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ------------------------------------------------------------- the work line
 // Item j of a sequence (rows 256 j ..) and head takes the blocks up to its
 // last row's token, and `setup` units more.
@@ -79,6 +99,9 @@ __device__ __forceinline__ int item_blocks(const Call& k, int len, int q, int j)
   return (len - q + last / k.group) / W_KEYS + 1;
 }
 __device__ __forceinline__ int items_of(const Call& k, int q) { return (q * k.group + W_ROWS - 1) / W_ROWS; }
+
+// what a block counts: with two tiles half as much again as with one (3.2 and 2.2 us)
+__device__ __forceinline__ int item_cost(const Call& k, int q, int j) { return q * k.group - j * W_ROWS > 128 ? 3 : 2; }
 
 __device__ __forceinline__ bool lay_out_wide(const Call& k, long long* pre, long long* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -97,7 +120,7 @@ __device__ __forceinline__ bool lay_out_wide(const Call& k, long long* pre, long
           if (report) set_device_err(DERR_KV8_ARGS);
         } else if (b <= k.rows) {
           const int items = items_of(k, q);
-          for (int j = 0; j < items; ++j) x += item_blocks(k, len, q, j) + k.setup;
+          for (int j = 0; j < items; ++j) x += item_blocks(k, len, q, j) * item_cost(k, q, j) + k.setup;
           x *= k.c.kvh;
         }
       }
@@ -130,6 +153,7 @@ struct Item {
   int slot, len, a, q, head, row0;  // row0: first of its rows
   int b0, b1, blocks;               // blocks [b0, b1) of `blocks` are this part's
   long long next;
+  int left;                         // units of it behind this part
 };
 __device__ __forceinline__ Item item_at(const Call& k, const long long* pre, long long at, long long end) {
   int lo = 0, hi = k.n;
@@ -143,10 +167,11 @@ __device__ __forceinline__ Item item_at(const Call& k, const long long* pre, lon
   p.a = k.cu[lo];
   p.q = k.cu[lo + 1] - p.a;
   long long rel = at - pre[lo];
-  int j = 0, size;
+  int j = 0, size, cost;
   for (;; ++j) {  // head after head within an item's rows
     p.blocks = item_blocks(k, p.len, p.q, j);
-    size = p.blocks + k.setup;
+    cost = item_cost(k, p.q, j);
+    size = p.blocks * cost + k.setup;
     if (rel < (long long)size * k.c.kvh) break;
     rel -= (long long)size * k.c.kvh;
   }
@@ -154,8 +179,9 @@ __device__ __forceinline__ Item item_at(const Call& k, const long long* pre, lon
   p.row0 = j * W_ROWS;
   const int u = (int)(rel - (long long)p.head * size);
   p.next = min(at - u + size, end);
-  p.b0 = max(0, u - k.setup);
-  p.b1 = max(0, (int)(p.next - at) + u - k.setup);
+  p.b0 = max(0, u - k.setup) / cost;
+  p.b1 = max(0, (int)(p.next - at) + u - k.setup) / cost;
+  p.left = (int)(at - u + size - p.next);
   return p;
 }
 
@@ -181,6 +207,13 @@ __device__ __forceinline__ void codes16_half(uint4 w, uint32_t f, uint32_t (&h)[
     }
   }
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -193,7 +226,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   constexpr int NS = S::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);  // NS, count 3 (converting warps)
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);  // NS, count W_CONV
   uint64_t* kv_empty = kv_full + NS;                                   // NS: both tiles' MMAs have read the stage
   uint64_t* q_full = kv_empty + NS;                                    // 2, count 4: the tile's Q is in shared memory
   uint64_t* s_full = q_full + 2;                                       // 2: S in TMEM
@@ -211,7 +244,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   pdl_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], 3);
+      mbar_init(&kv_full[s], W_CONV);
       mbar_init(&kv_empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -239,8 +272,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
 
-  if (warp < 4) {
-    regs_down<104>();
+  if (warp < 4 || warp >= 12) {
+    regs_down<W_REGS_LOW>();
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------- MMA issuer
@@ -272,7 +305,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           const Item p = item_at(k, pre, at, end);
           const int rows = p.q * k.group - p.row0;
           if (p.b0 == 0 && p.b1 > 0 && p.b1 < p.blocks) {
-            join_parts = (int)((p.next + p.blocks - p.b1 - 1) / per) - blockIdx.x + 1;
+            join_parts = (int)((p.next + p.left - 1) / per) - blockIdx.x + 1;
             Join j;
             j.parts = join_parts, j.tile_rows = min(W_ROWS, rows), j.row0 = p.row0, j.head = p.head, j.a = p.a;
             k.join[blockIdx.x] = j;
@@ -324,8 +357,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       }
     } else {
       // ------------------------------------------------ converting warps
-      constexpr int PER_ROW = D / 16, LOADS = (512 + 95) / 96;
-      const int pt = threadIdx.x - 32;
+      // A unit is 32 pieces of 512 bytes: 512 / D consecutive tokens' codes, 16 bytes for each lane.
+      constexpr int ROWS = 512 / D, PER_SIDE = W_KEYS / ROWS, LOADS = (32 + W_CONV - 1) / W_CONV;
+      const int cw = warp < 4 ? warp - 1 : warp - 9;
+      const int lrow = lane / (D / 16), lq = lane % (D / 16);
       uint32_t g = 0;
       bool ok = true;
       const long page_stride = c.page_bytes();
@@ -337,86 +372,95 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         const int32_t* table = c.table + (long)p.slot * c.max_pages;
         const uint8_t* head_base = c.codes + ((long)k.layer * 2 * c.kvh + p.head) * c.ps * D;
         const int per_block = W_KEYS >> c.ps_log2;  // pages of a block
-        // lane x: page x of a block, and its scales (0: behind the last token)
-        struct Pages {
-          int pg;
-          float ks, vs;
-        };
-        auto pages = [&](int blk) {
-          Pages x = {0, 0.f, 0.f};
+        // Loads run a block ahead: the codes of block j + 1, the scales of its
+        // pages and the page ids of block j + 2 are requested before block j
+        // is converted.  The processor counts a warp's open loads in a few
+        // counters that it shares among them, so waiting for an old load may
+        // wait for a new one: `after` makes every new address depend on what
+        // the old loads brought (by a zero that the compiler does not know).
+        auto page_id = [&](int blk) {  // lane x: page x of the block; -1 behind the last token
           const int tok = blk * W_KEYS + (lane << c.ps_log2);
-          if (lane < per_block && tok < p.len) {
-            x.pg = table[tok >> c.ps_log2];
-            if (c.page_ok(x.pg)) {
-              x.ks = c.scales[c.unit(x.pg, k.layer, 0, p.head)];
-              x.vs = c.scales[c.unit(x.pg, k.layer, 1, p.head)];
-            } else {
-              set_device_err(DERR_KV8_TABLE);
-              x.pg = 0;
-              x.ks = x.vs = __uint_as_float(NAN_SCALE);
-            }
-          }
-          return x;
+          return lane < per_block && tok < p.len ? table[tok >> c.ps_log2] : -1;
+        };
+        auto scale_of = [&](int page, int side) {  // 0 behind the last token
+          if (page == -1) return 0.f;
+          return c.page_ok(page) ? c.scales[c.unit(page, k.layer, side, p.head)] : __uint_as_float(NAN_SCALE);
         };
         uint4 nx[LOADS];
-        auto load = [&](int pg, int blk, int unit) {  // 8 KB of codes: this thread's pieces; zeros behind the last token
-          const int side = unit >= S::UNITS / 2, part = unit - side * (S::UNITS / 2);
-          const uint8_t* src = head_base + side * side_stride;
-#pragma unroll
-          for (int e = 0; e < LOADS; ++e) {
-            const int i = pt + 96 * e, row = min(i / PER_ROW, S::UNIT_ROWS - 1) + part * S::UNIT_ROWS;
-            const int page = __shfl_sync(0xffffffffu, pg, row >> c.ps_log2);
-            nx[e] = make_uint4(0, 0, 0, 0);
-            if (i < 512 && blk * W_KEYS + row < p.len)
-              nx[e] = __ldcg(reinterpret_cast<const uint4*>(src + page * page_stride + ((row & (c.ps - 1)) * D + (i % PER_ROW) * 16)));
-          }
+        auto load = [&](int e, int w, int page, int blk, int unit, uint32_t after) {  // zeros behind the last token
+          const int i = w + W_CONV * e + 32 * unit;  // piece of the block
+          const int side = i >= PER_SIDE, row0 = (i & (PER_SIDE - 1)) * ROWS;
+          const int pg = __shfl_sync(0xffffffffu, page, (row0 >> c.ps_log2) & 31);
+          nx[e] = make_uint4(0, 0, 0, 0);
+          if (w + W_CONV * e < 32 && blk * W_KEYS + row0 + lrow < p.len && c.page_ok(pg))
+            nx[e] = __ldcg(reinterpret_cast<const uint4*>(head_base + pg * page_stride + (side ? side_stride : 0) +
+                                                          ((row0 & (c.ps - 1)) * D + lane * 16 + after)));
         };
         float vref = 0.f;
-        Pages now = pages(p.b0);
-        load(now.pg, p.b0, 0);
+        int page = page_id(p.b0), page1 = p.b0 + 1 < p.b1 ? page_id(p.b0 + 1) : -1;
+        if (page < -1 || page >= c.num_pages) set_device_err(DERR_KV8_TABLE);
+        float ks = scale_of(page, 0), vs = scale_of(page, 1);
+#pragma unroll
+        for (int e = 0; e < LOADS; ++e) load(e, cw, page, p.b0, 0, 0);
         for (int j = p.b0; j < p.b1; ++j, ++g) {
           const int s = g % NS;
-          Pages next = {0, 0.f, 0.f};
-          if (j + 1 < p.b1) next = pages(j + 1);
           // factors of the block's pages
-          const bool nan = !(now.ks <= 3.0e38f && now.vs <= 3.0e38f);
-          const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(now.ks)))));
-          const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(now.vs)))));
+          const bool nan = !(ks <= 3.0e38f && vs <= 3.0e38f);
+          const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(ks)))));
+          const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(vs)))));
           vref = fmaxf(vref, vmax);
-          const float kr = now.ks * (1.f / kmax), vr = now.vs * (1.f / vref);
+          const float kr = ks * (1.f / kmax), vr = vs * (1.f / vref);
           // a page with a scale that is not a number: its keys are not, its values 0 (only rows that see it notice)
           const uint32_t kf = nan ? 0x7e007e00u : half2_of(kr, kr), vf = nan ? 0u : half2_of(vr, vr);
           if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((g / NS) & 1u) ^ 1u))) {
             ok = false;
             break;
           }
-          if (pt == 0) info[s] = make_float2(kmax, vref);
+          const bool odd = __any_sync(0xffffffffu, nan);
+          if (cw == 0 && lane == 0) info[s] = make_float2(odd ? -kmax : kmax, vref);
+          if (page1 < -1 || page1 >= c.num_pages) set_device_err(DERR_KV8_TABLE);
 #pragma unroll
           for (int u = 0; u < S::UNITS; ++u) {
+            const bool same = u + 1 < S::UNITS;
             uint4 cur[LOADS];
-#pragma unroll
-            for (int e = 0; e < LOADS; ++e) cur[e] = nx[e];
-            if (u + 1 < S::UNITS) load(now.pg, j, u + 1);
-            else if (j + 1 < p.b1) load(next.pg, j + 1, 0);
-            const int side = u >= S::UNITS / 2, part = u - side * (S::UNITS / 2);
-            const uint32_t dst = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE);
+            uint32_t after = page1 | kf | vf;
 #pragma unroll
             for (int e = 0; e < LOADS; ++e) {
-              const int i = pt + 96 * e, row = min(i / PER_ROW, S::UNIT_ROWS - 1) + part * S::UNIT_ROWS, q = i % PER_ROW;
-              const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row >> c.ps_log2);
+              cur[e] = nx[e];
+              after |= cur[e].x | cur[e].y | cur[e].z | cur[e].w;
+            }
+            after &= k.zero;
+            int w = cw;
+            asm volatile("" : "+r"(w));  // the pieces' offsets are formed anew here: kept, they would cost registers
+            if (same) {
+#pragma unroll
+              for (int e = 0; e < LOADS; ++e) load(e, w, page, j, u + 1, after);
+            } else if (j + 1 < p.b1) {
+#pragma unroll
+              for (int e = 0; e < LOADS; ++e) load(e, w, page1, j + 1, 0, after);
+              ks = scale_of(page1, 0);
+              vs = scale_of(page1, 1);
+              page = page1;
+              page1 = j + 2 < p.b1 ? page_id(j + 2 + after) : -1;
+            }
+            const uint32_t dst = smem_u32(smem + S::KV_OFF + 2 * s * S::TILE);
+#pragma unroll
+            for (int e = 0; e < LOADS; ++e) {
+              const int i = w + W_CONV * e + 32 * u;
+              const int side = i >= PER_SIDE, row0 = (i & (PER_SIDE - 1)) * ROWS, row = row0 + lrow;
+              const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, (row0 >> c.ps_log2) & 31);
               uint32_t h[8];
               codes16_half<FMT>(cur[e], f, h);
-              if (i < 512) {
+              if (w + W_CONV * e < 32) {
                 // the two 16-byte pieces in an order that keeps eight lanes in different banks
-                const bool x = D == 128 && ((q >> 2) & 1);
-                const uint32_t tile = dst + (D == 128 ? (q >> 2) * 16384 : 0);
-                const uint32_t a0 = tile + sw128(row, (2 * q) & 7), a1 = tile + sw128(row, (2 * q + 1) & 7);
-                sts128(x ? a1 : a0, x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2], x ? h[7] : h[3]);
-                sts128(x ? a0 : a1, x ? h[0] : h[4], x ? h[1] : h[5], x ? h[2] : h[6], x ? h[3] : h[7]);
+                const bool x = D == 128 && (lq >> 2);
+                const uint32_t tile = dst + side * S::TILE + (row >> 3) * 1024 + (row & 7) * 128 + (D == 128 ? (lq >> 2) * 16384 : 0);
+                const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
+                sts128(tile + (x ? c0 ^ 16 : c0), x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2], x ? h[7] : h[3]);
+                sts128(tile + (x ? c0 : c0 ^ 16), x ? h[0] : h[4], x ? h[1] : h[5], x ? h[2] : h[6], x ? h[3] : h[7]);
               }
             }
           }
-          now = next;
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&kv_full[s]);
@@ -426,7 +470,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
     }
   } else {
     // -------------------------------------------------- softmax of a tile
-    regs_up<200>();
+    regs_up<W_REGS_HIGH>();
     const int a = (warp >> 2) - 1, qw = warp & 3, r = qw * 32 + lane;
     const uint32_t tl = tmem + a * 256 + ((uint32_t)(qw * 32) << 16);
     const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
@@ -486,24 +530,45 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         tc_fence_after();
         const volatile float2* at_info = &info[g % NS];
         const float2 scale = make_float2(at_info->x, at_info->y);
-        const float fs = fmaxf(scale.x * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
-        uint32_t v[W_KEYS];
-        tmem_ld64(tl, v);
-        tmem_ld64(tl + 64, v + 64);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (D == 64 && lane == 0) mbar_arrive(&s_free[a]);
-        if (j * W_KEYS + W_KEYS - 1 > first_pos) {
-#pragma unroll
-          for (int e = 0; e < W_KEYS; ++e)
-            if (j * W_KEYS + e > pos) v[e] = __float_as_uint(-INFINITY);
-        }
+        const float fs = fmaxf(fabsf(scale.x) * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
+        const bool edge = j * W_KEYS + W_KEYS - 1 > first_pos;
+        const int last = pos - j * W_KEYS;  // the last key of the block that the row sees
+        // The scores are read in quarters of 32; the last two twice, for the
+        // maximum and for the weights.  With all 128 kept in registers the
+        // other warps would have too few (spilled, each load would wait).
         float mx8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[i]);
+        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+        uint32_t x[3][32];
+        auto masked = [&](uint32_t (&v)[32], int q) {
+          if (edge) {
 #pragma unroll
-        for (int e = 8; e < W_KEYS; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(v[e]));
+            for (int e = 0; e < 32; ++e)
+              if (32 * q + e > last) v[e] = __float_as_uint(-INFINITY);
+          }
+        };
+        auto maximum = [&](uint32_t (&v)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float& y = mx8[(e >> 1) & 7];
+            y = fmax3(y, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          }
+        };
+        tmem_ld32(tl + 64, x[0]);
+        tmem_ld32(tl + 96, x[1]);
+        tmem_wait_ld();
+        masked(x[0], 2);
+        maximum(x[0]);
+        tmem_ld32(tl, x[0]);
+        masked(x[1], 3);
+        maximum(x[1]);
+        tmem_ld32(tl + 32, x[1]);
+        tmem_wait_ld();
+        tmem_ld32(tl + 64, x[2]);
+        masked(x[0], 0);
+        maximum(x[0]);
+        masked(x[1], 1);
+        maximum(x[1]);
         const float mx = fs * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                     fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
         // the reference moves when a row passes it by 2^8, and O also when the value scale rises
@@ -521,38 +586,67 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           vref = scale.y;
         }
         const float off = m == -INFINITY ? 0.f : m - 6.f;  // weights up to 2^14 in f16, down to 2^-30 of the reference
-        float rs8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rs8[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < W_KEYS; e += 2) {
-          const float p0 = ex2f(fmaf(__uint_as_float(v[e]), fs, -off));
-          const float p1 = ex2f(fmaf(__uint_as_float(v[e + 1]), fs, -off));
-          rs8[e & 7] += p0;
-          rs8[(e + 1) & 7] += p1;
-          v[e >> 1] = half2_of(p0, p1);
+        // P's place is free, and O complete, once the block before has been multiplied
+        if (j > p.b0 && !warp_wait(&pv_done[a], (t - 1) & 1u)) {
+          ok = false;
+          break;
         }
-        l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
-        if (j > p.b0) {
-          if (!warp_wait(&pv_done[a], (t - 1) & 1u)) {
-            ok = false;
-            break;
+        tc_fence_after();
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 fs2 = make_float2(fs, fs), off2 = make_float2(-off, -off);
+        // one pair in four goes through the FMA pipe, unless the block has masked scores or ones that are not numbers
+        const bool all_mufu = edge || scale.x < 0.f;
+        auto weights = [&](uint32_t (&v)[32], int q, bool mufu) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fs2, off2);
+            if (!mufu && (e & 6) == 6)
+              z = ex2_fma2(make_float2(fmaxf(z.x, -126.f), fmaxf(z.y, -126.f)));
+            else
+              z = make_float2(ex2f(z.x), ex2f(z.y));
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
+            y[e >> 1] = half2_of(z.x, z.y);
           }
-          tc_fence_after();
-          if (rescale) {
+          tmem_st16(tl + S::T_P + 16 * q, y);
+        };
+        auto release = [&]() {  // S is read: the next block's scores may be formed meanwhile
+          if (D == 64) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[a]);
+          }
+        };
+        if (all_mufu) {
+          weights(x[0], 0, true);
+          tmem_ld32(tl + 96, x[0]);
+          weights(x[1], 1, true);
+          tmem_wait_ld();
+          release();
+          masked(x[2], 2);
+          weights(x[2], 2, true);
+          masked(x[0], 3);
+          weights(x[0], 3, true);
+        } else {
+          weights(x[0], 0, false);
+          tmem_ld32(tl + 96, x[0]);
+          weights(x[1], 1, false);
+          tmem_wait_ld();
+          release();
+          weights(x[2], 2, false);
+          weights(x[0], 3, false);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (j > p.b0 && rescale) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(tl + S::T_O + q * 32, o);
-              tmem_wait_ld();
+          for (int q = 0; q < D / 32; ++q) {
+            tmem_ld32(tl + S::T_O + q * 32, x[0]);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tl + S::T_O + q * 32, o);
-            }
+            for (int i = 0; i < 32; ++i) x[0][i] = __float_as_uint(__uint_as_float(x[0][i]) * alpha);
+            tmem_st32(tl + S::T_O + q * 32, x[0]);
           }
         }
-        tmem_st32(tl + S::T_P, v);
-        tmem_st32(tl + S::T_P + 32, v + 32);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -641,8 +735,10 @@ static inline size_t wide_workspace_bytes(const Cache& c) {
   return (size_t)sm_count() * (sizeof(Join) + 2 * (size_t)W_ROWS * (c.d + 2) * 4);
 }
 
+// The streaming kernel for the call's short sequences starts on the SMs that
+// the wide kernel leaves; each kernel of the chain ends after the one before it.
 template <int FMT, int D>
-static inline cudaError_t wide_launch(const Call& k, void* work, cudaStream_t st) {
+static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_work, cudaStream_t st) {
   using S = Wide<D>;
   static DeviceOnce once;
   cudaError_t e = run_once_per_device(once, [] {
@@ -653,18 +749,21 @@ static inline cudaError_t wide_launch(const Call& k, void* work, cudaStream_t st
   Call a = k;
   a.join = static_cast<Join*>(work);
   a.part = reinterpret_cast<float*>(a.join + grid);
-  a.setup = 2;
-  a.min_part = 4;
+  a.setup = 5;
+  a.min_part = 11;
   wide_kernel<FMT, D><<<grid, W_THREADS, S::bytes(k.n), st>>>(a);
   e = cudaGetLastError();
+  if (e == cudaSuccess && k.narrow) e = stream(k, stream_work, st, true);
   if (e != cudaSuccess) return e;
   return launch_after(join_wide_kernel<D>, dim3(grid, W_ROWS / 32), 256, 0, st, a);
 }
 
-static inline cudaError_t wide(const Call& k, void* work, cudaStream_t st) {
+static inline cudaError_t wide(const Call& k, void* work, void* stream_work, cudaStream_t st) {
   if (k.c.fmt == GPT2_KV_INT8)
-    return k.c.d == 64 ? wide_launch<GPT2_KV_INT8, 64>(k, work, st) : wide_launch<GPT2_KV_INT8, 128>(k, work, st);
-  return k.c.d == 64 ? wide_launch<GPT2_KV_E4M3, 64>(k, work, st) : wide_launch<GPT2_KV_E4M3, 128>(k, work, st);
+    return k.c.d == 64 ? wide_launch<GPT2_KV_INT8, 64>(k, work, stream_work, st)
+                       : wide_launch<GPT2_KV_INT8, 128>(k, work, stream_work, st);
+  return k.c.d == 64 ? wide_launch<GPT2_KV_E4M3, 64>(k, work, stream_work, st)
+                     : wide_launch<GPT2_KV_E4M3, 128>(k, work, stream_work, st);
 }
 
 // ---------------------------------------------------------------- the call
@@ -677,9 +776,8 @@ static inline int narrow_limit(int group, int n, int max_q) {
 
 static inline size_t attention_workspace_bytes(const Cache& c, int H, int n, int, int max_q) {
   const int group = H / c.kvh;
-  const size_t a = narrow_limit(group, n, max_q) ? stream_workspace_bytes(c, H, max_q) : 0;
-  const size_t b = (long)group * max_q > NARROW_ROWS ? wide_workspace_bytes(c) : 0;
-  return a > b ? a : b;  // the kernels run one after the other
+  return (narrow_limit(group, n, max_q) ? stream_workspace_bytes(c, H, max_q) : 0) +
+         ((long)group * max_q > NARROW_ROWS ? wide_workspace_bytes(c) : 0);
 }
 
 static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, long ldq, bf16* out, long ldo,
@@ -704,11 +802,9 @@ static inline cudaError_t attention(const Cache& c, int layer, const bf16* q, lo
   k.part = nullptr;
   k.narrow = narrow_limit(k.group, n, max_q);
   k.setup = k.min_part = 0;
-  if (k.narrow) {
-    const cudaError_t e = stream(k, work, st);
-    if (e != cudaSuccess) return e;
-  }
-  return (long)k.group * max_q > NARROW_ROWS ? wide(k, work, st) : cudaSuccess;
+  k.zero = 0;
+  if ((long)k.group * max_q <= NARROW_ROWS) return stream(k, work, st, false);
+  return wide(k, work, static_cast<uint8_t*>(work) + wide_workspace_bytes(c), st);
 }
 
 }  // namespace kv8

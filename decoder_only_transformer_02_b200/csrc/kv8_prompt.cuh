@@ -10,15 +10,16 @@
 // and the result is O / sum P as in the streaming kernel (kv8_attention.cuh).
 //
 // The tensor cores read f16 from shared memory, the cache holds 8-bit codes, so
-// seven warps convert each block on its way: the codes of the next 16 KB are
+// four warps convert each block on its way: the codes of the next 16 KB are
 // loaded while these 16 KB are converted and stored as swizzled f16 tiles.  A
 // key block's values are code * scale / (the block's largest scale), exact in
 // f16 unless 2^15 or more below it; the largest scale multiplies the scores.
 // Values are taken relative to the largest scale so far; when that rises, O is
 // scaled down as it is when the row maximum moves.
 //
-// Roles (512 threads, one CTA per SM, some registers moved to the softmax): warp 0 issues the MMAs of both tiles, warps 1-3 and 12-15
-// convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1.  Two tiles per
+// Roles (512 threads, one CTA per SM, some registers moved to the softmax):
+// warps 0-3 convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warp
+// 12 issues the MMAs of both.  Two tiles per
 // CTA instead of two CTAs of one tile: the conversion is done once for both,
 // and one tile's exponentials run while the other's MMAs do.
 //
@@ -34,10 +35,11 @@
 namespace kv8 {
 
 constexpr int W_THREADS = 512;
-constexpr int W_CONV = 7;    // converting warps
-// registers of a thread: 8 softmax warps and 8 others share the 16 * 32 * 128 of the launch
-constexpr int W_REGS_LOW = 112, W_REGS_HIGH = 144;
-static_assert(W_REGS_LOW + W_REGS_HIGH == 2 * 128, "the launch's registers, no more");
+constexpr int W_CONV = 4;    // converting warps
+// Registers of a thread: the launch gives every warp W_REGS; the warpgroups
+// (converting, softmax twice, MMA) share them out anew.
+constexpr int W_REGS = 128, W_REGS_CONV = 128, W_REGS_SOFT = 144, W_REGS_MMA = 96;
+static_assert(W_REGS_CONV + 2 * W_REGS_SOFT + W_REGS_MMA <= 4 * W_REGS, "the launch's registers, no more");
 constexpr int W_ROWS = 256;  // rows of a work item (two tiles)
 constexpr int W_KEYS = 128;  // keys of a block
 
@@ -47,9 +49,10 @@ struct Wide {
   static constexpr int TILE = 128 * D * 2;               // one f16 tile: Q, K or V
   static constexpr int KV_OFF = 2 * TILE;                // after the two Q tiles; stage s: K, V
   static constexpr int BAR_OFF = KV_OFF + NS * 2 * TILE;
-  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale (negative: some page's is not a number), value scale so far
+  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale, value scale so far
   static constexpr int LINE_OFF = INFO_OFF + 256;
   static constexpr int UNITS = D / 64;                   // 16 KB units of codes in a block: all of it, or keys, values
+  static constexpr int HALVES = 2 / UNITS;               // sides in a unit
   // TMEM columns of a tile: S, P (in place of S's first 64 when d = 128), O
   static constexpr uint32_t T_P = D == 64 ? 128 : 0, T_O = D == 64 ? 192 : 128;
   static size_t bytes(int n) { return LINE_OFF + (size_t)(n + 1) * 8 + 1024; }
@@ -67,20 +70,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-// 2^x of two values on the FMA and integer pipes (MUFU's 16 a cycle are what
-// the softmax waits for): n = x to the nearest integer by adding 1.5 * 2^23,
-// 2^(x - n) from a polynomial of degree 4 fitted here to the least largest
-// relative error on [-1/2, 1/2] (2.7e-6), n added to the exponent.  x from -126 to 126.
-__device__ __forceinline__ float2 ex2_fma2(float2 x) {
-  const float2 big = make_float2(12582912.f, 12582912.f);
-  const float2 t = add2(x, big), f = sub2(x, sub2(t, big));
-  float2 y = fma2(make_float2(0.009570102207362652f, 0.009570102207362652f), f, make_float2(0.05591786280274391f, 0.05591786280274391f));
-  y = fma2(y, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  y = fma2(y, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  y = fma2(y, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
 // f16 instruction descriptor: fp32 accumulate, M = 128; A K-major, B K-major or MN-major
 __host__ __device__ constexpr uint32_t f16_idesc(int n, int b_mn) {
@@ -207,12 +196,10 @@ __device__ __forceinline__ void codes16_half(uint4 w, uint32_t f, uint32_t (&h)[
     }
   }
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -257,7 +244,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -272,10 +259,9 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
 
-  if (warp < 4 || warp >= 12) {
-    regs_down<W_REGS_LOW>();
-    if (warp == 0) {
-      if (lane == 0) {
+  if (warp >= 12) {
+    regs_down<W_REGS_MMA>();
+    if (threadIdx.x == 384) {
         // ---------------------------------------------------- MMA issuer
         constexpr uint32_t id_s = f16_idesc(W_KEYS, 0), id_pv = f16_idesc(D, 1);
         uint32_t g = 0, t[2] = {0, 0}, items[2] = {0, 0};
@@ -354,12 +340,12 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
         tc_commit(drain);
         if (!mbar_wait_drain(drain, 0)) set_device_err(DERR_WAIT_TIMEOUT);
-      }
-    } else {
+    }
+  } else if (warp < 4) {
       // ------------------------------------------------ converting warps
-      // A unit is 32 pieces of 512 bytes: 512 / D consecutive tokens' codes, 16 bytes for each lane.
-      constexpr int ROWS = 512 / D, PER_SIDE = W_KEYS / ROWS, LOADS = (32 + W_CONV - 1) / W_CONV;
-      const int cw = warp < 4 ? warp - 1 : warp - 9;
+      // A unit is 32 pieces of 512 bytes: 512 / D consecutive tokens' codes, 16
+      // bytes for each lane; warp w takes the pieces w, w + 4, ...
+      constexpr int ROWS = 512 / D, NX = 32 / W_CONV, PARTS = NX / S::HALVES;  // parts of a side that a warp takes in a unit
       const int lrow = lane / (D / 16), lq = lane % (D / 16);
       uint32_t g = 0;
       bool ok = true;
@@ -378,34 +364,37 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         // counters that it shares among them, so waiting for an old load may
         // wait for a new one: `after` makes every new address depend on what
         // the old loads brought (by a zero that the compiler does not know).
-        auto page_id = [&](int blk) {  // lane x: page x of the block; -1 behind the last token
-          const int tok = blk * W_KEYS + (lane << c.ps_log2);
-          return lane < per_block && tok < p.len ? table[tok >> c.ps_log2] : -1;
+        // What lies behind the last token is read (of its last page) and
+        // cleared before it is converted.
+        const int last_page = c.pages_of(p.len) - 1;
+        auto page_id = [&](int blk) {  // lane x: page x of the block
+          return table[min(blk * per_block + min(lane, per_block - 1), last_page)];
         };
-        auto scale_of = [&](int page, int side) {  // 0 behind the last token
-          if (page == -1) return 0.f;
-          return c.page_ok(page) ? c.scales[c.unit(page, k.layer, side, p.head)] : __uint_as_float(NAN_SCALE);
-        };
-        uint4 nx[LOADS];
-        auto load = [&](int e, int w, int page, int blk, int unit, uint32_t after) {  // zeros behind the last token
-          const int i = w + W_CONV * e + 32 * unit;  // piece of the block
-          const int side = i >= PER_SIDE, row0 = (i & (PER_SIDE - 1)) * ROWS;
-          const int pg = __shfl_sync(0xffffffffu, page, (row0 >> c.ps_log2) & 31);
-          nx[e] = make_uint4(0, 0, 0, 0);
-          if (w + W_CONV * e < 32 && blk * W_KEYS + row0 + lrow < p.len && c.page_ok(pg))
-            nx[e] = __ldcg(reinterpret_cast<const uint4*>(head_base + pg * page_stride + (side ? side_stride : 0) +
-                                                          ((row0 & (c.ps - 1)) * D + lane * 16 + after)));
+        auto valid = [&](int page) { return c.page_ok(page) ? page : 0; };
+        uint4 nx[NX];
+        // the warp's pieces of a unit: HALVES sides x PARTS runs of rows
+        auto load = [&](int page, int unit, uint32_t after) {
+#pragma unroll
+          for (int e = 0; e < PARTS; ++e) {
+            const int row0 = (warp + W_CONV * e) * ROWS;
+            const int pg = __shfl_sync(0xffffffffu, page, row0 >> c.ps_log2);
+            const uint8_t* src = head_base + pg * page_stride + ((row0 & (c.ps - 1)) * D + lane * 16 + after);
+#pragma unroll
+            for (int h = 0; h < S::HALVES; ++h)
+              nx[e * S::HALVES + h] = __ldcg(reinterpret_cast<const uint4*>(src + (S::HALVES == 2 ? h : unit) * side_stride));
+          }
         };
         float vref = 0.f;
-        int page = page_id(p.b0), page1 = p.b0 + 1 < p.b1 ? page_id(p.b0 + 1) : -1;
-        if (page < -1 || page >= c.num_pages) set_device_err(DERR_KV8_TABLE);
-        float ks = scale_of(page, 0), vs = scale_of(page, 1);
-#pragma unroll
-        for (int e = 0; e < LOADS; ++e) load(e, cw, page, p.b0, 0, 0);
+        int page = page_id(p.b0), page1 = page_id(p.b0 + 1);
+        bool bad = !c.page_ok(page);
+        page = valid(page);
+        float ks = c.scales[c.unit(page, k.layer, 0, p.head)], vs = c.scales[c.unit(page, k.layer, 1, p.head)];
+        load(page, 0, 0);
         for (int j = p.b0; j < p.b1; ++j, ++g) {
           const int s = g % NS;
           // factors of the block's pages
-          const bool nan = !(ks <= 3.0e38f && vs <= 3.0e38f);
+          if (bad) set_device_err(DERR_KV8_TABLE);
+          const bool nan = bad || !(ks <= 3.0e38f && vs <= 3.0e38f);
           const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(ks)))));
           const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(vs)))));
           vref = fmaxf(vref, vmax);
@@ -416,48 +405,46 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
             ok = false;
             break;
           }
-          const bool odd = __any_sync(0xffffffffu, nan);
-          if (cw == 0 && lane == 0) info[s] = make_float2(odd ? -kmax : kmax, vref);
-          if (page1 < -1 || page1 >= c.num_pages) set_device_err(DERR_KV8_TABLE);
+          if (warp == 0 && lane == 0) info[s] = make_float2(kmax, vref);
+          const int left = p.len - j * W_KEYS;  // tokens from the block on
 #pragma unroll
           for (int u = 0; u < S::UNITS; ++u) {
-            const bool same = u + 1 < S::UNITS;
-            uint4 cur[LOADS];
+            uint4 cur[NX];
             uint32_t after = page1 | kf | vf;
 #pragma unroll
-            for (int e = 0; e < LOADS; ++e) {
+            for (int e = 0; e < NX; ++e) {
               cur[e] = nx[e];
               after |= cur[e].x | cur[e].y | cur[e].z | cur[e].w;
             }
             after &= k.zero;
-            int w = cw;
-            asm volatile("" : "+r"(w));  // the pieces' offsets are formed anew here: kept, they would cost registers
-            if (same) {
-#pragma unroll
-              for (int e = 0; e < LOADS; ++e) load(e, w, page, j, u + 1, after);
+            if (u + 1 < S::UNITS) {
+              load(page, u + 1, after);
             } else if (j + 1 < p.b1) {
-#pragma unroll
-              for (int e = 0; e < LOADS; ++e) load(e, w, page1, j + 1, 0, after);
-              ks = scale_of(page1, 0);
-              vs = scale_of(page1, 1);
-              page = page1;
-              page1 = j + 2 < p.b1 ? page_id(j + 2 + after) : -1;
+              bad = !c.page_ok(page1);
+              page = valid(page1);
+              load(page, 0, after);
+              ks = c.scales[c.unit(page, k.layer, 0, p.head)];
+              vs = c.scales[c.unit(page, k.layer, 1, p.head)];
+              page1 = page_id(j + 2 + after);
             }
-            const uint32_t dst = smem_u32(smem + S::KV_OFF + 2 * s * S::TILE);
 #pragma unroll
-            for (int e = 0; e < LOADS; ++e) {
-              const int i = w + W_CONV * e + 32 * u;
-              const int side = i >= PER_SIDE, row0 = (i & (PER_SIDE - 1)) * ROWS, row = row0 + lrow;
-              const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, (row0 >> c.ps_log2) & 31);
-              uint32_t h[8];
-              codes16_half<FMT>(cur[e], f, h);
-              if (w + W_CONV * e < 32) {
+            for (int e = 0; e < PARTS; ++e) {
+              const int row0 = (warp + W_CONV * e) * ROWS, row = row0 + lrow;
+              const uint32_t rows = smem_u32(smem + S::KV_OFF + 2 * s * S::TILE) + (row >> 3) * 1024 + (row & 7) * 128;
+              const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
+#pragma unroll
+              for (int h = 0; h < S::HALVES; ++h) {
+                const int side = S::HALVES == 2 ? h : u;
+                const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row0 >> c.ps_log2);
+                uint4 w = cur[e * S::HALVES + h];
+                if (left < W_KEYS && row >= left) w = make_uint4(0, 0, 0, 0);
+                uint32_t x[8];
+                codes16_half<FMT>(w, f, x);
                 // the two 16-byte pieces in an order that keeps eight lanes in different banks
-                const bool x = D == 128 && (lq >> 2);
-                const uint32_t tile = dst + side * S::TILE + (row >> 3) * 1024 + (row & 7) * 128 + (D == 128 ? (lq >> 2) * 16384 : 0);
-                const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
-                sts128(tile + (x ? c0 ^ 16 : c0), x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2], x ? h[7] : h[3]);
-                sts128(tile + (x ? c0 : c0 ^ 16), x ? h[0] : h[4], x ? h[1] : h[5], x ? h[2] : h[6], x ? h[3] : h[7]);
+                const bool y = D == 128 && (lq >> 2);
+                const uint32_t tile = rows + side * S::TILE + (D == 128 ? (lq >> 2) * 16384 : 0);
+                sts128(tile + (y ? c0 ^ 16 : c0), y ? x[4] : x[0], y ? x[5] : x[1], y ? x[6] : x[2], y ? x[7] : x[3]);
+                sts128(tile + (y ? c0 : c0 ^ 16), y ? x[0] : x[4], y ? x[1] : x[5], y ? x[2] : x[6], y ? x[3] : x[7]);
               }
             }
           }
@@ -467,10 +454,9 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         }
       }
       if (!ok && lane == 0) set_device_err(DERR_WAIT_TIMEOUT);
-    }
   } else {
     // -------------------------------------------------- softmax of a tile
-    regs_up<W_REGS_HIGH>();
+    regs_up<W_REGS_SOFT>();
     const int a = (warp >> 2) - 1, qw = warp & 3, r = qw * 32 + lane;
     const uint32_t tl = tmem + a * 256 + ((uint32_t)(qw * 32) << 16);
     const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
@@ -487,9 +473,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       if (p.b1 == p.b0) continue;
       const bool on = r < rows;
       const int row = p.row0 + a * 128 + (on ? r : 0), tok = row / k.group, h = p.head * k.group + row - tok * k.group;
-      const int pos = p.len - p.q + tok;  // the last token the row sees
-      // the tile's first row sees the fewest
-      const int first_pos = p.len - p.q + (p.row0 + a * 128) / k.group;
+      // the last token that the row sees, and the tile's first row, which sees the fewest, from this part's first block on
+      int last = p.len - p.q + tok - p.b0 * W_KEYS;
+      int first_last = p.len - p.q + (p.row0 + a * 128) / k.group - p.b0 * W_KEYS;
+      const bool whole = p.b0 == 0 && p.b1 == p.blocks, begins = p.b0 == 0;
+      const int out_row = p.a + tok;
       // ---- Q: the row times a power of two, as f16
       float rowf;
       {
@@ -522,7 +510,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         if (lane == 0) mbar_arrive(&q_full[a]);
       }
       float m = -INFINITY, l = 0.f, vref = 0.f;
-      for (int j = p.b0; j < p.b1; ++j, ++g, ++t) {
+      const int blocks = p.b1 - p.b0;
+      for (int j = 0; j < blocks; ++j, ++g, ++t, last -= W_KEYS, first_last -= W_KEYS) {
         if (!warp_wait(&s_full[a], t & 1u)) {
           ok = false;
           break;
@@ -530,9 +519,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         tc_fence_after();
         const volatile float2* at_info = &info[g % NS];
         const float2 scale = make_float2(at_info->x, at_info->y);
-        const float fs = fmaxf(fabsf(scale.x) * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
-        const bool edge = j * W_KEYS + W_KEYS - 1 > first_pos;
-        const int last = pos - j * W_KEYS;  // the last key of the block that the row sees
+        const float fs = fmaxf(scale.x * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
+        const bool edge = first_last < W_KEYS - 1;
         // The scores are read in quarters of 32; the last two twice, for the
         // maximum and for the weights.  With all 128 kept in registers the
         // other warps would have too few (spilled, each load would wait).
@@ -587,57 +575,43 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         }
         const float off = m == -INFINITY ? 0.f : m - 6.f;  // weights up to 2^14 in f16, down to 2^-30 of the reference
         // P's place is free, and O complete, once the block before has been multiplied
-        if (j > p.b0 && !warp_wait(&pv_done[a], (t - 1) & 1u)) {
+        if (j > 0 && !warp_wait(&pv_done[a], (t - 1) & 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 fs2 = make_float2(fs, fs), off2 = make_float2(-off, -off);
-        // one pair in four goes through the FMA pipe, unless the block has masked scores or ones that are not numbers
-        const bool all_mufu = edge || scale.x < 0.f;
-        auto weights = [&](uint32_t (&v)[32], int q, bool mufu) {
-          uint32_t y[16];
+        auto weights = [&](uint32_t (&v)[32], int q) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fs2, off2);
-            if (!mufu && (e & 6) == 6)
-              z = ex2_fma2(make_float2(fmaxf(z.x, -126.f), fmaxf(z.y, -126.f)));
-            else
+          for (int half = 0; half < 2; ++half) {
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int e = 16 * half + 2 * i;
+              float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fs2, off2);
               z = make_float2(ex2f(z.x), ex2f(z.y));
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
-            y[e >> 1] = half2_of(z.x, z.y);
-          }
-          tmem_st16(tl + S::T_P + 16 * q, y);
-        };
-        auto release = [&]() {  // S is read: the next block's scores may be formed meanwhile
-          if (D == 64) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[a]);
+              sum[i & 1] = add2(sum[i & 1], z);
+              y[i] = half2_of(z.x, z.y);
+            }
+            tmem_st8(tl + S::T_P + 16 * q + 8 * half, y);
           }
         };
-        if (all_mufu) {
-          weights(x[0], 0, true);
-          tmem_ld32(tl + 96, x[0]);
-          weights(x[1], 1, true);
-          tmem_wait_ld();
-          release();
-          masked(x[2], 2);
-          weights(x[2], 2, true);
-          masked(x[0], 3);
-          weights(x[0], 3, true);
-        } else {
-          weights(x[0], 0, false);
-          tmem_ld32(tl + 96, x[0]);
-          weights(x[1], 1, false);
-          tmem_wait_ld();
-          release();
-          weights(x[2], 2, false);
-          weights(x[0], 3, false);
+        weights(x[0], 0);
+        tmem_ld32(tl + 96, x[0]);
+        weights(x[1], 1);
+        tmem_wait_ld();
+        if (D == 64) {  // S is read: the next block's scores may be formed meanwhile
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[a]);
         }
+        masked(x[2], 2);
+        weights(x[2], 2);
+        masked(x[0], 3);
+        weights(x[0], 3);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (j > p.b0 && rescale) {
+        if (j > 0 && rescale) {
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             tmem_ld32(tl + S::T_O + q * 32, x[0]);
@@ -658,8 +632,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       }
       tc_fence_after();
       // ---- the item's result, or this part's share of it
-      const bool whole = p.b0 == 0 && p.b1 == p.blocks;
-      float* part = k.part + ((long)blockIdx.x * 2 + (p.b0 == 0)) * W_ROWS * (D + 2);
+      float* part = k.part + ((long)blockIdx.x * 2 + begins) * W_ROWS * (D + 2);
       const int pr = a * 128 + r;
       const float M = m - 6.f;  // the sums' reference
       const float f = whole ? vref / l : vref;
@@ -669,7 +642,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         tmem_ld32(tl + S::T_O + q * 32, o);
         tmem_wait_ld();
         if (on && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(k.out + (long)(p.a + tok) * k.ldo + h * D + q * 32);
+          uint4* dst = reinterpret_cast<uint4*>(k.out + (long)out_row * k.ldo + h * D + q * 32);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f),
@@ -689,46 +662,61 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         part[W_ROWS * D + pr] = M;
         part[W_ROWS * D + W_ROWS + pr] = l;
       }
-      if (on && whole && k.lse) k.lse[(long)(p.a + tok) * k.H + h] = (M + log2f(l)) * 0.6931471805599453f;
+      if (on && whole && k.lse) k.lse[(long)out_row * k.H + h] = (M + log2f(l)) * 0.6931471805599453f;
     }
     if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 12) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
-// CTA (x, y): rows 32 y .. of the item that begins in part x and goes on after it.
+// CTA (x, y): rows J_ROWS y .. of the item that begins in part x and goes on
+// after it, four columns of a row per thread; four parts are requested at once.
+constexpr int J_ROWS = 16;
 template <int D>
-__global__ void __launch_bounds__(256) join_wide_kernel(const Call k) {
+__global__ void __launch_bounds__(J_ROWS * D / 4) join_wide_kernel(const Call k) {
   pdl_wait();
   const Join t = k.join[blockIdx.x];
-  if (t.parts == 0) return;
+  const int r = blockIdx.y * J_ROWS + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
+  if (r >= t.tile_rows || t.parts == 0) return;
   constexpr long SIZE = (long)W_ROWS * (D + 2);
   const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
-  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
-    const int r = blockIdx.y * 32 + i / (D / 4), d4 = i % (D / 4);
-    if (r >= t.tile_rows) break;
-    float M = -INFINITY, L = 0.f;
-    for (int j = 0; j < t.parts; ++j) M = fmaxf(M, first[(j ? (2 * j - 1) * SIZE : 0) + W_ROWS * D + r]);
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int j = 0; j < t.parts; ++j) {
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < t.parts; j0 += 4) {
+    float m[4], l[4];
+    float4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
       const float* src = first + (j ? (2 * j - 1) * SIZE : 0);
-      const float f = ex2_approx(src[W_ROWS * D + r] - Mu);
-      const float4 x = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
-      L += f * src[W_ROWS * D + W_ROWS + r];
-      a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
+      m[u] = -INFINITY, l[u] = 0.f, x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < t.parts) {
+        m[u] = src[W_ROWS * D + r];
+        l[u] = src[W_ROWS * D + W_ROWS + r];
+        x[u] = *reinterpret_cast<const float4*>(src + r * D + 4 * d4);
+      }
     }
-    const float inv = 1.f / L;
-    const int row = t.row0 + r, tok = row / k.group, h = t.head * k.group + row - tok * k.group;
-    *reinterpret_cast<uint2*>(k.out + (long)(t.a + tok) * k.ldo + h * D + 4 * d4) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    if (d4 == 0 && k.lse) k.lse[(long)(t.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
+    const float nm = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+    const float nu = nm == -INFINITY ? 0.f : nm;
+    const float f = ex2_approx(M - nu);
+    M = nm;
+    L *= f, a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float h = ex2_approx(m[u] - nu);
+      L += h * l[u];
+      a.x += h * x[u].x, a.y += h * x[u].y, a.z += h * x[u].z, a.w += h * x[u].w;
+    }
   }
+  const float inv = 1.f / L;
+  const int row = t.row0 + r, tok = row / k.group, h = t.head * k.group + row - tok * k.group;
+  *reinterpret_cast<uint2*>(k.out + (long)(t.a + tok) * k.ldo + h * D + 4 * d4) =
+      make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  if (d4 == 0 && k.lse) k.lse[(long)(t.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 static inline size_t wide_workspace_bytes(const Cache& c) {
@@ -742,6 +730,11 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   using S = Wide<D>;
   static DeviceOnce once;
   cudaError_t e = run_once_per_device(once, [] {
+    // a warp that asks for registers that the launch does not have would wait for good
+    cudaFuncAttributes at;
+    cudaError_t r = cudaFuncGetAttributes(&at, wide_kernel<FMT, D>);
+    if (r != cudaSuccess) return r;
+    if (at.numRegs != W_REGS) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(wide_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes(MAX_SEQS));
   });
   if (e != cudaSuccess) return e;
@@ -755,7 +748,7 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   e = cudaGetLastError();
   if (e == cudaSuccess && k.narrow) e = stream(k, stream_work, st, true);
   if (e != cudaSuccess) return e;
-  return launch_after(join_wide_kernel<D>, dim3(grid, W_ROWS / 32), 256, 0, st, a);
+  return launch_after(join_wide_kernel<D>, dim3(grid, W_ROWS / J_ROWS), J_ROWS * D / 4, 0, st, a);
 }
 
 static inline cudaError_t wide(const Call& k, void* work, void* stream_work, cudaStream_t st) {

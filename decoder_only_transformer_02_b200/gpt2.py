@@ -405,7 +405,8 @@ class KV8Cache:
     def __init__(self, codes, scales, table, lens, refs):
         import torch
         fmts = {torch.int8: GPT2_KV_INT8, torch.float8_e4m3fn: GPT2_KV_E4M3}
-        self._torch = torch
+        self._torch, self._i32, self._f32, self._bf16 = torch, torch.int32, torch.float32, torch.bfloat16
+        self._only_device = torch.cuda.device_count() == 1
         dev = codes.device
         shapes_ok = codes.dim() == 6 and codes.shape[2] == 2 and codes.dtype in fmts and dev.type == "cuda" and \
             scales.dtype == torch.float32 and tuple(scales.shape) == tuple(codes.shape[:4]) and \
@@ -447,7 +448,7 @@ class KV8Cache:
         return int(self._lib.gpt2_kv8_attention_workspace_bytes(self._p, n_head, n, rows, max_q))
 
     def _call(self, what, fn, *args):
-        if self._torch.cuda.current_device() == self.device.index:
+        if self._only_device or self._torch.cuda.current_device() == self.device.index:
             r = fn(*args)
         else:
             with self._torch.cuda.device(self.device):
@@ -455,78 +456,86 @@ class KV8Cache:
         if r != 0:
             raise GPT2Error(r, what)
 
-    def _ints(self, what, *tensors):
-        i32, dev = self._torch.int32, self.device
-        for t in tensors:
-            if t.dtype is not i32 or t.device != dev or t.dim() != 1 or not t.is_contiguous():
-                raise GPT2Error(-1, what + ": index arrays are contiguous one-dimensional int32 tensors on the cache's device")
+    def _ints(self, what, t):
+        """Length of an index array."""
+        if t.dtype is not self._i32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous():
+            raise GPT2Error(-1, what + ": index arrays are contiguous one-dimensional int32 tensors on the cache's device")
+        return len(t)
 
-    def _work(self, what, work):
-        if work.device != self.device or not work.is_contiguous():
+    def _work(self, what, t):
+        if t.device != self.device or not t.is_contiguous():
             raise GPT2Error(-1, what + ": work is a contiguous tensor on the cache's device")
-        return work.data_ptr(), work.numel() * work.element_size()
+        return t.data_ptr(), t.nbytes
 
     def _rows(self, what, t, heads):
-        """Row stride of a bf16 [rows, heads, head_dim] view whose rows are contiguous."""
-        if t.dtype is not self._torch.bfloat16 or t.device != self.device or t.dim() != 3 or t.shape[1] != heads or \
-                t.shape[2] != self.head_dim or t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
-            raise GPT2Error(-1, what + ": rows are bf16 [rows, heads, head_dim] with contiguous heads on the cache's device")
-        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * self.head_dim)
+        """Rows, and row stride, of a bf16 [rows, heads, head_dim] view whose rows are contiguous."""
+        if t.dtype is self._bf16 and t.device == self.device and t.dim() == 3:
+            n, h, d = t.shape
+            s0, s1, s2 = t.stride()
+            if h == heads and d == self.head_dim and s2 == 1 and (s1 == d or h == 1):
+                return n, (s0 if n > 1 else max(s0, h * d))
+        raise GPT2Error(-1, what + ": rows are bf16 [rows, heads, head_dim] with contiguous heads on the cache's device")
 
     def resize(self, slots, new_lens, work, stream=None):
         """slots[i] to the length new_lens[i] (device int32); 0 frees the slot."""
-        self._ints("gpt2_kv8_resize", slots, new_lens)
-        if slots.shape != new_lens.shape:
-            raise GPT2Error(-1, "gpt2_kv8_resize: one length for each slot")
-        w, nb = self._work("gpt2_kv8_resize", work)
-        self._call("gpt2_kv8_resize", self._lib.gpt2_kv8_resize, self._p, slots.data_ptr(), new_lens.data_ptr(),
-                   slots.shape[0], w, nb, _stream_ptr(stream))
+        what = "gpt2_kv8_resize"
+        n = self._ints(what, slots)
+        if self._ints(what, new_lens) != n:
+            raise GPT2Error(-1, what + ": one length for each slot")
+        w, nb = self._work(what, work)
+        self._call(what, self._lib.gpt2_kv8_resize, self._p, slots.data_ptr(), new_lens.data_ptr(), n, w, nb,
+                   _stream_ptr(stream))
 
     def fork(self, src, dst, work, stream=None):
         """The empty slots dst[i] take over the tokens of src[i] (device int32)."""
-        self._ints("gpt2_kv8_fork", src, dst)
-        if src.shape != dst.shape:
-            raise GPT2Error(-1, "gpt2_kv8_fork: one destination for each source")
-        w, nb = self._work("gpt2_kv8_fork", work)
-        self._call("gpt2_kv8_fork", self._lib.gpt2_kv8_fork, self._p, src.data_ptr(), dst.data_ptr(), src.shape[0], w,
-                   nb, _stream_ptr(stream))
+        what = "gpt2_kv8_fork"
+        n = self._ints(what, src)
+        if self._ints(what, dst) != n:
+            raise GPT2Error(-1, what + ": one destination for each source")
+        w, nb = self._work(what, work)
+        self._call(what, self._lib.gpt2_kv8_fork, self._p, src.data_ptr(), dst.data_ptr(), n, w, nb,
+                   _stream_ptr(stream))
 
     def compact(self, work, live=None, stream=None):
         """Pages in use to the lowest ids; live: device int32 [1] that receives their number."""
-        if live is not None:
-            self._ints("gpt2_kv8_compact", live)
-        w, nb = self._work("gpt2_kv8_compact", work)
-        self._call("gpt2_kv8_compact", self._lib.gpt2_kv8_compact, self._p, _ptr(live), w, nb, _stream_ptr(stream))
+        what = "gpt2_kv8_compact"
+        if live is not None and self._ints(what, live) < 1:
+            raise GPT2Error(-1, what + ": live holds one number")
+        w, nb = self._work(what, work)
+        self._call(what, self._lib.gpt2_kv8_compact, self._p, _ptr(live), w, nb, _stream_ptr(stream))
 
     def append(self, layer, k, v, slots, cu, stream=None):
         """k, v: bf16 [rows, n_kv_head, head_dim], of the same row stride (views
         of a fused projection will do); rows cu[i]..cu[i+1]-1 are the last
         tokens of slots[i]."""
-        self._ints("gpt2_kv8_append", slots, cu)
-        ld = self._rows("gpt2_kv8_append", k, self.n_kv_head)
-        if v.shape != k.shape or self._rows("gpt2_kv8_append", v, self.n_kv_head) != ld or \
-                cu.shape[0] != slots.shape[0] + 1:
-            raise GPT2Error(-1, "gpt2_kv8_append: k and v have one shape and stride, cu one offset more than slots")
-        self._call("gpt2_kv8_append", self._lib.gpt2_kv8_append, self._p, layer, k.data_ptr(), v.data_ptr(), ld,
-                   slots.data_ptr(), cu.data_ptr(), slots.shape[0], k.shape[0], _stream_ptr(stream))
+        what = "gpt2_kv8_append"
+        n = self._ints(what, slots)
+        shape = self._rows(what, k, self.n_kv_head)
+        if self._rows(what, v, self.n_kv_head) != shape or self._ints(what, cu) != n + 1:
+            raise GPT2Error(-1, what + ": k and v have one shape and stride, cu one offset more than slots")
+        self._call(what, self._lib.gpt2_kv8_append, self._p, layer, k.data_ptr(), v.data_ptr(), shape[1],
+                   slots.data_ptr(), cu.data_ptr(), n, shape[0], _stream_ptr(stream))
 
     def attention(self, layer, q, out, slots, cu, max_q, work, lse=None, stream=None):
         """Causal attention of q (bf16 [rows, n_head, head_dim], views with a row
         stride will do) over the cached tokens into out (the same shape); lse:
         None or float32 [rows, n_head].  No sequence has more than max_q rows."""
         what = "gpt2_kv8_attention"
-        self._ints(what, slots, cu)
-        rows, heads = q.shape[0], q.shape[1]
-        ldq, ldo = self._rows(what, q, heads), self._rows(what, out, heads)
-        if out.shape[0] != rows or cu.shape[0] != slots.shape[0] + 1:
+        n = self._ints(what, slots)
+        heads = q.shape[1] if q.dim() == 3 else 0
+        rows, ldq = self._rows(what, q, heads)
+        out_rows, ldo = self._rows(what, out, heads)
+        if out_rows != rows or self._ints(what, cu) != n + 1:
             raise GPT2Error(-1, what + ": out has q's shape, cu one offset more than slots")
-        if lse is not None and (lse.dtype is not self._torch.float32 or lse.device != self.device or
-                                tuple(lse.shape) != (rows, heads) or not lse.is_contiguous()):
-            raise GPT2Error(-1, what + ": lse is a contiguous float32 [rows, n_head] on the cache's device")
+        p_lse = None
+        if lse is not None:
+            if lse.dtype is not self._f32 or lse.device != self.device or lse.shape != (rows, heads) or \
+                    not lse.is_contiguous():
+                raise GPT2Error(-1, what + ": lse is a contiguous float32 [rows, n_head] on the cache's device")
+            p_lse = lse.data_ptr()
         w, nb = self._work(what, work)
-        self._call(what, self._lib.gpt2_kv8_attention, self._p, layer, q.data_ptr(), ldq, out.data_ptr(), ldo,
-                   _ptr(lse), heads, slots.data_ptr(), cu.data_ptr(), slots.shape[0], rows, max_q, w, nb,
-                   _stream_ptr(stream))
+        self._call(what, self._lib.gpt2_kv8_attention, self._p, layer, q.data_ptr(), ldq, out.data_ptr(), ldo, p_lse,
+                   heads, slots.data_ptr(), cu.data_ptr(), n, rows, max_q, w, nb, _stream_ptr(stream))
 
 
 def check_device_error(stream=None):

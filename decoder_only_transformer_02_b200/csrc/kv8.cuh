@@ -87,8 +87,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
 template <int FMT>
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   if (FMT == GPT2_KV_E4M3) return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
-  const int x = __float2int_rn(a), y = __float2int_rn(b), z = __float2int_rn(c), w = __float2int_rn(d);
-  return (uint32_t)(x & 255) | ((uint32_t)(y & 255) << 8) | ((uint32_t)(z & 255) << 16) | ((uint32_t)w << 24);
+  // adding 1.5 * 2^23 rounds to the nearest integer (even on ties), in the low bits
+  const uint32_t x = __float_as_uint(a + 12582912.f), y = __float_as_uint(b + 12582912.f);
+  const uint32_t z = __float_as_uint(c + 12582912.f), w = __float_as_uint(d + 12582912.f);
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 template <int FMT>
 __device__ __forceinline__ void unpack4(uint32_t w, float (&f)[4]) {
@@ -105,12 +107,17 @@ __device__ __forceinline__ void unpack4(uint32_t w, float (&f)[4]) {
 
 constexpr int APPEND_WARPS = 8;
 
-// CTA (x, y): x names a run of one sequence's new tokens inside one page, y a
-// group of APPEND_WARPS of the 2 * kvh (side, head) pairs, one warp each.
+// CTA (x, y): x names a run of one sequence's new tokens inside one page, whose
+// 2 * kvh (side, head) pairs the warps of the CTAs (x, *) share.
 // by_row: x is a row, and works if its token is the run's first.  Otherwise x
 // counts runs: sequence i owns the numbers from cu[i] / ps + 2 i, enough since
 // its q tokens touch at most q / ps + 2 pages; no prefix sum is needed.
-template <int FMT>
+// HELD: 16-byte pieces of a tile that a lane keeps between the two passes (the
+// rest is read again): 1 for short runs, 4 (a tile of 1024 values) for prompts.
+// What it moves: 2 bytes in, 1 out per value.  15,400 rows of 2 x 768 values:
+// 17.8 us (3.9 TB/s; 25.7 with both passes reading, 22 with 8 pieces held, whose
+// registers cost half the warps); 256 single rows: 5.8 us, its chain of loads.
+template <int FMT, int HELD>
 __global__ void __launch_bounds__(32 * APPEND_WARPS)
     append_kernel(Cache c, int layer, const bf16* __restrict__ k, const bf16* __restrict__ v, long ld,
                   const int32_t* __restrict__ slots, const int32_t* __restrict__ cu, int n, int rows, int by_row) {
@@ -120,6 +127,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
   if (tid == 0) s_i = -1;
   __syncthreads();
   bool bad = false;
+#pragma unroll 1
   for (int i = tid; i < n; i += blockDim.x) {
     const int a = cu[i], b = cu[i + 1];
     const bool mine = by_row ? x >= a && x < b
@@ -136,6 +144,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
   const int a = s_a, q = s_b - a, slot = s_slot;
   // a slot named twice: the later entries are refused, or both would write the same tokens
   bool twice = false;
+#pragma unroll 1
   for (int j = tid; j < i; j += blockDim.x) twice |= slots[j] == slot && cu[j + 1] > cu[j];
   twice = __syncthreads_or(twice);
   if (q == 0) return;
@@ -155,75 +164,99 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
     if (pos >= len) return;
   }
   end = min(len, (pos | (c.ps - 1)) + 1);
-  const int pair = blockIdx.y * APPEND_WARPS + warp;
-  if (pair >= 2 * c.kvh) return;
-  const int side = pair >= c.kvh, head = pair - side * c.kvh;
   const int page = c.table[(long)slot * c.max_pages + (pos >> c.ps_log2)];
   if (!c.page_ok(page)) {
-    if (lane == 0) set_device_err(DERR_KV8_TABLE);
+    if (tid == 0) set_device_err(DERR_KV8_TABLE);
     return;
   }
-  const long u = c.unit(page, layer, side, head);
   const int d8 = c.d >> 3, m = end - pos;       // 16-byte pieces of a row; rows
   const int per = 32 / d8, sub = lane / d8;     // rows a warp reads at once; this lane's
-  const bf16* src = (side ? v : k) + (long)(a + pos - p0) * ld + head * c.d + (lane % d8) * 8;
-  // pass 1: the largest magnitude, as bf16 bits (their order is the values')
-  uint32_t mx = 0;
-  for (int r = sub; r < m; r += per) {
-    const uint4 w = *reinterpret_cast<const uint4*>(src + (long)r * ld);
-    const uint32_t t0 = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
-    const uint32_t t1 = __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
-    mx = __vmaxu2(mx, __vmaxu2(t0, t1));
-  }
-  mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
   const int off = pos & (c.ps - 1);
-  uint32_t bits = scale_bits_for(mx, FMT);
-  uint8_t* tile = c.codes + u * c.tile();
-  if (off != 0) {
-    const uint32_t old = __float_as_uint(c.scales[u]);
-    if (bits > old && bits != NAN_SCALE) {  // positive floats and the NaN order as their bits
-      const float ratio = __uint_as_float(old) * inverse_pow2(bits);
-      for (int t = lane; t < (int)(c.tile() >> 4); t += 32) {
-        uint4 w = reinterpret_cast<uint4*>(tile)[t];
-        uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+  for (int pair = blockIdx.y * APPEND_WARPS + warp; pair < 2 * c.kvh; pair += gridDim.y * APPEND_WARPS) {
+    const int side = pair >= c.kvh, head = pair - side * c.kvh;
+    const long u = c.unit(page, layer, side, head);
+    const bf16* src = (side ? v : k) + (long)(a + pos - p0) * ld + head * c.d + (lane % d8) * 8;
+    uint8_t* tile = c.codes + u * c.tile();
+    // the largest magnitude, as bf16 bits (their order is the values')
+    uint4 x[HELD];
+    uint32_t mx = 0;
+    auto largest = [&](const uint4& w) {
+      const uint32_t t0 = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+      const uint32_t t1 = __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+      mx = __vmaxu2(mx, __vmaxu2(t0, t1));
+    };
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float f[4];
-          unpack4<FMT>(e[g], f);
-          e[g] = pack4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-        }
-        reinterpret_cast<uint4*>(tile)[t] = make_uint4(e[0], e[1], e[2], e[3]);
-      }
+    for (int i = 0; i < HELD; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (sub + i * per < m) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (long)(sub + i * per) * ld));
     }
-    bits = max(bits, old);
-  }
-  __syncwarp();  // every lane has read the old scale, and the rescaled codes come before the new ones
-  if (lane == 0) c.scales[u] = __uint_as_float(bits);
-  const float inv = bits >= NAN_SCALE ? 0.f : inverse_pow2(bits);
-  const bool nan = bits >= NAN_SCALE;
-  // pass 2: the codes
-  uint8_t* dst = tile + (long)off * c.d + (lane % d8) * 8;
-  for (int r = sub; r < m; r += per) {
-    const uint4 w = *reinterpret_cast<const uint4*>(src + (long)r * ld);
-    const float2 f0 = unpack_bf16x2(w.x), f1 = unpack_bf16x2(w.y), f2 = unpack_bf16x2(w.z), f3 = unpack_bf16x2(w.w);
-    uint2 o;
-    o.x = pack4<FMT>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
-    o.y = pack4<FMT>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
-    if (nan) o = make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(dst + (long)r * c.d) = o;
+    const uint32_t old = off ? __float_as_uint(c.scales[u]) : 0u;
+#pragma unroll 1
+    for (int r = sub + HELD * per; r < m; r += per) largest(__ldg(reinterpret_cast<const uint4*>(src + (long)r * ld)));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) largest(x[i]);
+    mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    uint32_t bits = scale_bits_for(mx, FMT);
+    if (off != 0) {
+      if (bits > old && bits != NAN_SCALE) {  // positive floats and the NaN order as their bits
+        const float ratio = __uint_as_float(old) * inverse_pow2(bits);
+#pragma unroll 1
+        for (int t = lane; t < (int)(c.tile() >> 4); t += 32) {
+          uint4 w = reinterpret_cast<uint4*>(tile)[t];
+          uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float f[4];
+            unpack4<FMT>(e[g], f);
+            e[g] = pack4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+          }
+          reinterpret_cast<uint4*>(tile)[t] = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+      }
+      bits = max(bits, old);
+    }
+    __syncwarp();  // every lane has read the old scale, and the rescaled codes come before the new ones
+    if (lane == 0) c.scales[u] = __uint_as_float(bits);
+    const bool nan = bits >= NAN_SCALE;
+    const float inv = nan ? 0.f : inverse_pow2(bits);
+    uint8_t* dst = tile + (long)off * c.d + (lane % d8) * 8;
+    auto store = [&](const uint4& w, int r) {
+      const float2 f0 = unpack_bf16x2(w.x), f1 = unpack_bf16x2(w.y), f2 = unpack_bf16x2(w.z), f3 = unpack_bf16x2(w.w);
+      uint2 o;
+      o.x = pack4<FMT>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
+      o.y = pack4<FMT>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
+      if (nan) o = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(dst + r * c.d) = o;
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (sub + i * per < m) store(x[i], sub + i * per);
+#pragma unroll 1
+    for (int r = sub + HELD * per; r < m; r += per) store(__ldg(reinterpret_cast<const uint4*>(src + (long)r * ld)), r);
+    __syncwarp();
   }
 }
 
+constexpr long APPEND_CTAS = 148 * 4;
 static inline cudaError_t append(const Cache& c, int layer, const bf16* k, const bf16* v, long ld,
                                  const int32_t* slots, const int32_t* cu, int n, int rows, cudaStream_t st) {
   if (n == 0 || rows == 0) return cudaSuccess;
   const long runs = (long)(rows >> c.ps_log2) + 2L * n;
   const int by_row = rows <= runs;
-  const dim3 grid((unsigned)(by_row ? rows : runs), (2 * c.kvh + APPEND_WARPS - 1) / APPEND_WARPS);
+  const long xs = by_row ? rows : runs;
+  // finding its run costs a CTA four dependent loads: with runs enough for
+  // APPEND_CTAS, more of the pairs go to one CTA
+  const int most = (2 * c.kvh + APPEND_WARPS - 1) / APPEND_WARPS;
+  const int ys = (int)(xs * most <= APPEND_CTAS ? most : (APPEND_CTAS + xs - 1) / xs);
+  const dim3 grid((unsigned)xs, ys < 1 ? 1 : ys > most ? most : ys);
+#define KV8_APPEND(F, HELD) \
+  append_kernel<F, HELD><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row)
   if (c.fmt == GPT2_KV_INT8)
-    append_kernel<GPT2_KV_INT8><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row);
+    by_row ? KV8_APPEND(GPT2_KV_INT8, 1) : KV8_APPEND(GPT2_KV_INT8, 4);
   else
-    append_kernel<GPT2_KV_E4M3><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row);
+    by_row ? KV8_APPEND(GPT2_KV_E4M3, 1) : KV8_APPEND(GPT2_KV_E4M3, 4);
+#undef KV8_APPEND
   return cudaGetLastError();
 }
 
@@ -257,47 +290,48 @@ static inline Work work_of(void* w, int n, int num_pages) {
 static inline size_t workspace_bytes(int n, int num_pages) { return 4 * (HEAD + 3 * (size_t)n + 3 * (size_t)num_pages); }
 
 // exclusive prefix sum over the block; `total` receives the sum
-__device__ __forceinline__ int block_scan(int v, int& total, int* s_warp) {
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t& total, uint64_t* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // s_warp is free again
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
+  uint64_t w = s_warp[lane];  // every warp adds up the warps' sums
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    s_warp[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  __syncthreads();
-  total = s_warp[31];
-  return x - v + (warp ? s_warp[warp - 1] : 0);
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const uint64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return x - v + (warp ? before : 0);
+}
+
+// four page counts from p on (1 behind the pool's end)
+__device__ __forceinline__ int4 refs_at(const Cache& c, int p) {
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p + 3 < c.num_pages) return __ldcg(reinterpret_cast<const int4*>(c.refs + p));
+  if (p < c.num_pages) r.x = __ldcg(c.refs + p);
+  if (p + 1 < c.num_pages) r.y = __ldcg(c.refs + p + 1);
+  if (p + 2 < c.num_pages) r.z = __ldcg(c.refs + p + 2);
+  return r;
 }
 
 // The wanted lowest free pages (refs 0) into list; returns how many there are
 // (at least `want`, or all of them).
-__device__ __forceinline__ int find_free(const Cache& c, int want, int32_t* list, int* s_warp) {
-  int found = 0;
+__device__ __forceinline__ uint64_t find_free(const Cache& c, uint64_t want, int32_t* list, uint64_t* s_warp) {
+  uint64_t found = 0;
+  int4 r = refs_at(c, 4 * threadIdx.x);
   for (int base = 0; base < c.num_pages && found < want; base += 4 * PLAN_THREADS) {
     const int p = base + 4 * threadIdx.x;
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p + 3 < c.num_pages) {
-      r = __ldcg(reinterpret_cast<const int4*>(c.refs + p));
-    } else {
-      if (p < c.num_pages) r.x = __ldcg(c.refs + p);
-      if (p + 1 < c.num_pages) r.y = __ldcg(c.refs + p + 1);
-      if (p + 2 < c.num_pages) r.z = __ldcg(c.refs + p + 2);
-    }
-    int total;
-    int at = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), total, s_warp);
+    const int4 next = refs_at(c, p + 4 * PLAN_THREADS);
+    uint64_t total;
+    uint64_t at = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), total, s_warp);
     if (r.x == 0 && at < want) list[at] = p;
     at += r.x == 0;
     if (r.y == 0 && at < want) list[at] = p + 1;
@@ -306,6 +340,7 @@ __device__ __forceinline__ int find_free(const Cache& c, int want, int32_t* list
     at += r.z == 0;
     if (r.w == 0 && at < want) list[at] = p + 3;
     found += total;
+    r = next;
   }
   return found;
 }
@@ -338,18 +373,28 @@ __device__ __forceinline__ bool claim(const Cache& c, int slot, uint32_t* s_map)
   return !(atomicOr(&s_map[slot >> 5], 1u << (slot & 31)) >> (slot & 31) & 1u);
 }
 
+// Shared memory of a plan: the slots' bitmap, and for a resize each entry's
+// slot, pages kept and number of pages given back by the entries before.
+static inline size_t plan_smem(const Cache& c, int n, bool resize) {
+  return (size_t)((c.num_slots + 31) / 32 * 4 + 7) / 8 * 8 + (resize ? (size_t)n * 16 : 0);
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS)
     resize_plan_kernel(Cache c, const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int n, Work w) {
-  extern __shared__ uint32_t s_map[];
-  __shared__ int s_warp[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) uint32_t s_map[];
+  __shared__ uint64_t s_warp[32];
+  const int tid = threadIdx.x, words = (c.num_slots + 31) / 32;
+  uint64_t* s_first = reinterpret_cast<uint64_t*>(s_map + (words + 1) / 2 * 2);  // [n]
+  int2* s_entry = reinterpret_cast<int2*>(s_first + n);                          // [n]
   pdl_launch();
-  for (int i = tid; i < (c.num_slots + 31) / 32; i += PLAN_THREADS) s_map[i] = 0;
+  for (int i = tid; i < words; i += PLAN_THREADS) s_map[i] = 0;
   __syncthreads();
-  int err = 0, want = 0, copies = 0;
+  int err = 0;
+  uint64_t want = 0, back = 0;  // pages wanted (and copies, from bit 40 on); pages given back
   for (int base = 0; base < n; base += PLAN_THREADS) {
     const int i = base + tid;
-    int need = 0, copy = 0, src = 0;
+    uint64_t need = 0, drop = 0;
+    int copy = 0, src = 0;
     if (i < n) {
       const int slot = slots[i], new_len = lens[i];
       const int old_len = c.len_of(slot);
@@ -359,40 +404,43 @@ __global__ void __launch_bounds__(PLAN_THREADS)
         const Change h = change_of(c, slot, old_len, new_len);
         if (h.copy < 0) err = DERR_KV8_TABLE;
         copy = h.copy > 0, src = h.src;
-        need = copy + max(0, h.want - h.have);
+        need = ((uint64_t)copy << 40) + copy + max(0, h.want - h.have);
+        drop = max(0, h.have - h.want);
+        s_entry[i] = make_int2(slot, h.want);
       }
     }
-    int total;
-    const int at = want + block_scan(need, total, s_warp);
-    if (i < n) w.first[i] = at;
+    uint64_t total;
+    const uint64_t at = want + block_scan(need, total, s_warp);
     want += total;
-    const int k = copies + block_scan(copy, total, s_warp);
+    if (i < n) w.first[i] = (int)(at & 0x7fffffffu);  // (whole where the call goes on)
     if (copy) {
-      w.copy[2 * k] = src;
-      w.copy[2 * k + 1] = at;
+      w.copy[2 * (at >> 40)] = src;
+      w.copy[2 * (at >> 40) + 1] = w.first[i];
     }
-    copies += total;
+    const uint64_t before = back + block_scan(drop, total, s_warp);
+    back += total;
+    if (i < n) s_first[i] = before;
   }
-  // pages given back: every id is checked before the first count changes
-  int bad = 0;
-  if (__syncthreads_or(err) == 0) {
-    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
-      const int slot = slots[i], have = c.pages_of(c.lens[slot]);
-      for (int j = c.pages_of(lens[i]) + lane; j < have; j += 32)
-        if (!c.page_ok(c.table[(long)slot * c.max_pages + j])) bad = 1;
-    }
-    if (bad) err = DERR_KV8_TABLE;
-  }
+  const uint64_t copies = want >> 40;
+  want &= (1ull << 40) - 1;
   if (__syncthreads_or(err) != 0) {
     if (err) set_device_err(err);
     if (tid == 0) w.head[0] = 0;
     return;
   }
   for (int sign = -1; sign <= 1; sign += 2) {  // give back; a second time, with +1, only where too few are free
-    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
-      const int slot = slots[i], have = c.pages_of(c.lens[slot]);
-      for (int j = c.pages_of(lens[i]) + lane; j < have; j += 32)
-        atomicAdd(&c.refs[c.table[(long)slot * c.max_pages + j]], sign);
+    for (uint64_t r = tid; r < back; r += PLAN_THREADS) {
+      int lo = 0, hi = n;  // the entry of the r-th page given back
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= r) lo = mid; else hi = mid;
+      }
+      const int2 e = s_entry[lo];
+      const int page = c.table[(long)e.x * c.max_pages + e.y + (r - s_first[lo])];
+      if (c.page_ok(page))
+        atomicAdd(&c.refs[page], sign);
+      else
+        set_device_err(DERR_KV8_TABLE);
     }
     __syncthreads();
     if (sign > 0) {
@@ -407,20 +455,21 @@ __global__ void __launch_bounds__(PLAN_THREADS)
   }
   if (tid == 0) {
     w.head[0] = 1;
-    w.head[1] = copies;
-    w.head[2] = want;
+    w.head[1] = (int)copies;
+    w.head[2] = (int)want;
   }
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS)
     fork_plan_kernel(Cache c, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, Work w) {
-  extern __shared__ uint32_t s_map[];
-  __shared__ int s_warp[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) uint32_t s_map[];
+  __shared__ uint64_t s_warp[32];
+  const int tid = threadIdx.x;
   pdl_launch();
   for (int i = tid; i < (c.num_slots + 31) / 32; i += PLAN_THREADS) s_map[i] = 0;
   __syncthreads();
-  int err = 0, want = 0;
+  int err = 0;
+  uint64_t want = 0;
   for (int base = 0; base < n; base += PLAN_THREADS) {
     const int i = base + tid;
     int part = 0, page = 0;
@@ -431,10 +480,11 @@ __global__ void __launch_bounds__(PLAN_THREADS)
       } else if (len & (c.ps - 1)) {
         part = 1;
         page = c.table[(long)src[i] * c.max_pages + (len >> c.ps_log2)];
+        if (!c.page_ok(page)) err = DERR_KV8_TABLE;
       }
     }
-    int total;
-    const int at = want + block_scan(part, total, s_warp);
+    uint64_t total;
+    const int at = (int)(want + block_scan(part, total, s_warp));
     if (i < n) w.first[i] = at;
     if (part) {
       w.copy[2 * at] = page;
@@ -442,69 +492,59 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     }
     want += total;
   }
-  int bad = 0;
-  if (__syncthreads_or(err) == 0) {
-    for (int i = warp; i < n; i += PLAN_THREADS / 32) {
-      const int used = c.pages_of(c.lens[src[i]]);
-      for (int j = lane; j < used; j += 32)
-        if (!c.page_ok(c.table[(long)src[i] * c.max_pages + j])) bad = 1;
-    }
-    if (bad) err = DERR_KV8_TABLE;
+  bool ok = __syncthreads_or(err) == 0;
+  if (ok && find_free(c, want, w.list, s_warp) < want) {
+    ok = false;
+    if (tid == 0) err = DERR_KV8_PAGES;
   }
-  if (__syncthreads_or(err) == 0 && find_free(c, want, w.list, s_warp) < want && tid == 0) err = DERR_KV8_PAGES;
-  if (__syncthreads_or(err) != 0) {
-    if (err) set_device_err(err);
-    if (tid == 0) w.head[0] = 0;
-    return;
-  }
+  if (err) set_device_err(err);
   if (tid == 0) {
-    w.head[0] = 1;
-    w.head[1] = want;
-    w.head[2] = want;
+    w.head[0] = ok;
+    w.head[1] = (int)want;
+    w.head[2] = (int)want;
   }
 }
 
 // n_live = pages with refs > 0.  The j-th live page with an id of n_live or
-// more moves to the j-th free page below n_live.  high[live rank] and rank[id]
-// are written for the pages that move, list[j] for the holes.
+// more moves to the j-th free page below n_live.  high[live rank] is written
+// for the pages that move, rank[id] for all from n_live on (-1: free), list[j]
+// for the holes.
 __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Work w) {
-  __shared__ int s_warp[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint64_t s_warp[32];
+  const int tid = threadIdx.x;
   pdl_launch();
-  int err = 0;
-  for (int i = warp; i < c.num_slots; i += PLAN_THREADS / 32) {
-    const int len = c.len_of(i);
-    if (len < 0) err = DERR_KV8_ARGS;
-    const int used = len < 0 ? 0 : c.pages_of(len);
-    for (int j = lane; j < used; j += 32) {
-      const int page = c.table[(long)i * c.max_pages + j];
-      if (!c.page_ok(page) || c.refs[page] <= 0) err = DERR_KV8_TABLE;
-    }
+  uint64_t count = 0;
+  for (int p = 4 * tid; p < c.num_pages; p += 4 * PLAN_THREADS) {
+    const int4 r = refs_at(c, p);
+    count += (r.x > 0) + (p + 1 < c.num_pages && r.y > 0) + (p + 2 < c.num_pages && r.z > 0) + (p + 3 < c.num_pages && r.w > 0);
   }
-  if (__syncthreads_or(err) != 0) {
-    if (err) set_device_err(err);
-    if (tid == 0) w.head[0] = 0;
-    return;
-  }
-  int live = 0;
-  for (int p = tid; p < c.num_pages; p += PLAN_THREADS) live += c.refs[p] > 0;
-  block_scan(live, live, s_warp);
+  uint64_t total;
+  block_scan(count, total, s_warp);
+  const int live = (int)total;
   if (tid == 0 && live == c.num_pages) w.head[4] = live;
   int before = 0;
-  for (int base = 0; base < c.num_pages; base += PLAN_THREADS) {
-    const int p = base + tid;
-    const int is = p < c.num_pages && c.refs[p] > 0;
-    int total;
-    const int r = before + block_scan(is, total, s_warp);  // live pages below p
-    if (p < c.num_pages) {
-      if (p == live) w.head[4] = r;
-      if (p < live && !is) w.list[p - r] = p;
-      if (p >= live && is) {
-        w.high[r] = p;
-        w.rank[p] = r;
+  int4 r = refs_at(c, 4 * tid);
+  for (int base = 0; base < c.num_pages; base += 4 * PLAN_THREADS) {
+    const int p0 = base + 4 * tid;
+    const int4 next = refs_at(c, p0 + 4 * PLAN_THREADS);
+    const int v[4] = {r.x, r.y, r.z, r.w};
+    int is[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) is[e] = p0 + e < c.num_pages && v[e] > 0;
+    int at = before + (int)block_scan(is[0] + is[1] + is[2] + is[3], total, s_warp);  // live pages below p
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = p0 + e;
+      if (p < c.num_pages) {
+        if (p == live) w.head[4] = at;
+        if (p < live && !is[e]) w.list[p - at] = p;
+        if (p >= live) w.rank[p] = is[e] ? at : -1;
+        if (p >= live && is[e]) w.high[at] = p;
       }
+      at += is[e];
     }
-    before += total;
+    before += (int)total;
+    r = next;
   }
   __syncthreads();
   if (tid == 0) {
@@ -592,7 +632,10 @@ __global__ void __launch_bounds__(COPY_THREADS)
     for (int j = lane; j < whole; j += 32) {
       const int page = from[j];
       to[j] = page;
-      atomicAdd(&c.refs[page], 1);
+      if (c.page_ok(page))
+        atomicAdd(&c.refs[page], 1);
+      else
+        set_device_err(DERR_KV8_TABLE);
     }
     if (lane == 0 && (len & (c.ps - 1))) {
       const int page = w.list[w.first[i]];
@@ -619,9 +662,15 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_apply_kernel(Cache c, in
   }
   for (int i = me >> 5; i < c.num_slots; i += stride >> 5) {
     int32_t* row = c.table + (long)i * c.max_pages;
-    const int used = c.pages_of(c.lens[i]);
-    for (int j = lane; j < used; j += 32)
-      if (row[j] >= live) row[j] = w.list[w.rank[row[j]] - low];
+    const int len = c.len_of(i), used = len < 0 ? 0 : c.pages_of(len);
+    if (len < 0) set_device_err(DERR_KV8_ARGS);
+    for (int j = lane; j < used; j += 32) {
+      const int page = row[j], r = !c.page_ok(page) ? -1 : page < live ? 0 : w.rank[page];
+      if (r < 0)
+        set_device_err(DERR_KV8_TABLE);
+      else if (page >= live)
+        row[j] = w.list[r - low];
+    }
   }
   if (me == 0 && live_out) *live_out = live;
   copy_pages(c, moves, [&](int k, int& s, int& t) {
@@ -654,8 +703,14 @@ static inline cudaError_t resize(const Cache& c, const int32_t* slots, const int
                                  cudaStream_t st) {
   if (n == 0) return cudaSuccess;
   const Work w = work_of(work, n, c.num_pages);
-  resize_plan_kernel<<<1, PLAN_THREADS, (size_t)((c.num_slots + 31) / 32) * 4, st>>>(c, slots, lens, n, w);
-  const cudaError_t e = cudaGetLastError();
+  static DeviceOnce once;
+  cudaError_t e = run_once_per_device(once, [] {
+    return cudaFuncSetAttribute(resize_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                MAX_SLOTS / 8 + 8 + MAX_SEQS * 16);
+  });
+  if (e != cudaSuccess) return e;
+  resize_plan_kernel<<<1, PLAN_THREADS, plan_smem(c, n, true), st>>>(c, slots, lens, n, w);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(resize_apply_kernel, dim3(APPLY_CTAS), COPY_THREADS, 0, st, c, slots, lens, n, w);
 }
@@ -663,7 +718,7 @@ static inline cudaError_t fork(const Cache& c, const int32_t* src, const int32_t
                                cudaStream_t st) {
   if (n == 0) return cudaSuccess;
   const Work w = work_of(work, n, c.num_pages);
-  fork_plan_kernel<<<1, PLAN_THREADS, (size_t)((c.num_slots + 31) / 32) * 4, st>>>(c, src, dst, n, w);
+  fork_plan_kernel<<<1, PLAN_THREADS, plan_smem(c, n, false), st>>>(c, src, dst, n, w);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(fork_apply_kernel, dim3(APPLY_CTAS), COPY_THREADS, 0, st, c, src, dst, n, w);

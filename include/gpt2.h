@@ -256,7 +256,8 @@ size_t gpt2_matmul_workspace_bytes(int M, int N, int K);
  * graph and take effect in stream order; with n or rows 0 they do nothing.  The host checks sizes and pointers
  * (GPT2_EINVAL, nothing enqueued).  What only the device knows (slots,
  * lengths, row offsets, page ids, free pages) is checked there: a refused call
- * or sequence records GPT2_ECACHE, which gpt2_check_device_error (below, or
+ * or sequence, or a table entry outside the pool (which is passed over),
+ * records GPT2_ECACHE, which gpt2_check_device_error (below, or
  * the next syncing call of a model handle) returns; no kernel traps.  Calls
  * that overlap in time need a workspace each, and must not name the same
  * slots unless both only read (attention); resize, fork and compact change

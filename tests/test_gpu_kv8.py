@@ -455,20 +455,47 @@ def test_table_calls_refused_as_a_whole():
     p.compact()
 
 
-def test_table_entries_outside_the_pool_are_refused():
+def test_table_entries_outside_the_pool_are_passed_over():
+    """Recorded, and neither read nor counted; the partly kept page is checked before anything changes."""
     G = _g()
-    p = Pair(R.INT8)
-    p.append([0], [40])
+
+    def run(page, call):
+        p = Pair(R.INT8)
+        p.append([0, 1], [40, 33])
+        p.dev.table[0, 1] = page
+        before = [t.clone() for t in (p.dev.refs, p.dev.lens, p.dev.table)]
+        call(p)
+        with pytest.raises(G.GPT2Error) as e:
+            G.check_device_error()
+        assert e.value.name == "ECACHE"
+        return before, (p.dev.refs, p.dev.lens, p.dev.table)
+
     for page in (-1, 40, 1 << 30):
-        p.dev.table[0, 2] = page
-        state = [t.clone() for t in (p.dev.refs, p.dev.lens, p.dev.table)]
-        for call in (lambda: p.dev.resize(_i32([0]), _i32([35]), p.work), lambda: p.dev.resize(_i32([0]), _i32([0]), p.work),
-                     lambda: p.dev.fork(_i32([0]), _i32([1]), p.work), lambda: p.dev.compact(p.work)):
-            call()
-            with pytest.raises(G.GPT2Error) as e:
-                G.check_device_error()
-            assert e.value.name == "ECACHE"
-            assert all(torch.equal(a, b) for a, b in zip(state, (p.dev.refs, p.dev.lens, p.dev.table)))
+        old, new = run(page, lambda p: p.dev.resize(_i32([0]), _i32([25]), p.work))
+        assert all(torch.equal(a, b) for a, b in zip(old, new))
+        old, new = run(page, lambda p: p.dev.resize(_i32([0]), _i32([0]), p.work))
+        assert new[1][0] == 0 and new[0].sum() == old[0].sum() - 2
+        old, new = run(page, lambda p: p.dev.fork(_i32([0]), _i32([2]), p.work))
+        assert new[1][2] == 40 and new[0].sum() == old[0].sum() + 2
+        old, new = run(page, lambda p: p.dev.compact(p.work))
+        assert torch.equal(old[1], new[1]) and new[2][0, 1] == page and new[0].sum() == old[0].sum()
+
+
+def test_lengths_whose_pages_pass_32_bits_are_refused():
+    """2^23 pages wanted by each of 256 slots: as a whole, changing nothing."""
+    G = _g()
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    c = G.KV8Cache.allocate(R.INT8, 1, 1, 64, 16, 20, 300, 1)
+    big = G.KV8Cache(c.codes, c.scales, torch.empty(300, 1 << 23, dtype=torch.int32, device="cuda"), c.lens, c.refs)
+    work = torch.empty(big.workspace_bytes(300), dtype=torch.uint8, device="cuda")
+    slots = _i32(range(300))
+    for n in (255, 256, 300):
+        big.resize(slots[:n], _i32([16 << 23] * n), work)
+        with pytest.raises(G.GPT2Error) as e:
+            G.check_device_error()
+        assert e.value.name == "ECACHE"
+        assert torch.all(c.refs == 0) and torch.all(c.lens == 0)
 
 
 def test_pools_larger_than_one_scan():

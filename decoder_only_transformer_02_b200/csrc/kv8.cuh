@@ -52,6 +52,34 @@ struct Cache {
   }
 };
 
+// The caller's description as the kernels take it; false where a size or
+// pointer is out of its limits.
+static inline bool cache_of(const gpt2_kv8* k, Cache& c) {
+  if (!k || !k->d_codes || !k->d_scales || !k->d_table || !k->d_lens || !k->d_refs) return false;
+  if (k->format != GPT2_KV_INT8 && k->format != GPT2_KV_E4M3) return false;
+  if (k->n_layer < 1 || k->n_layer > 1024 || k->n_kv_head < 1 || k->n_kv_head > 1024) return false;
+  if (k->head_dim != 64 && k->head_dim != 128) return false;
+  if (k->page_size != 16 && k->page_size != 32 && k->page_size != 64 && k->page_size != 128) return false;
+  if (k->num_pages < 1 || k->num_pages > MAX_PAGES || k->num_slots < 1 || k->num_slots > MAX_SLOTS) return false;
+  if (k->max_pages < 1 || (long)k->max_pages * k->page_size > MAX_TOKENS) return false;
+  if ((reinterpret_cast<uintptr_t>(k->d_codes) & 15) || (reinterpret_cast<uintptr_t>(k->d_refs) & 15)) return false;
+  c.fmt = k->format;
+  c.L = k->n_layer;
+  c.kvh = k->n_kv_head;
+  c.d = k->head_dim;
+  c.ps = k->page_size;
+  c.ps_log2 = k->page_size == 16 ? 4 : k->page_size == 32 ? 5 : k->page_size == 64 ? 6 : 7;
+  c.num_pages = k->num_pages;
+  c.num_slots = k->num_slots;
+  c.max_pages = k->max_pages;
+  c.codes = (uint8_t*)k->d_codes;
+  c.scales = k->d_scales;
+  c.table = k->d_table;
+  c.lens = k->d_lens;
+  c.refs = k->d_refs;
+  return true;
+}
+
 // griddepcontrol: the second kernel of a pair is launched while the first
 // runs and waits here for its results
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -401,32 +401,6 @@ int gpt2_attention_backward_noalloc(const void* qkv, const void* out, const void
 }
 
 // ------------------------------------------------------- paged 8-bit cache
-static bool kv8_cache(const gpt2_kv8* k, kv8::Cache& c) {
-  if (!k || !k->d_codes || !k->d_scales || !k->d_table || !k->d_lens || !k->d_refs) return false;
-  if (k->format != GPT2_KV_INT8 && k->format != GPT2_KV_E4M3) return false;
-  if (k->n_layer < 1 || k->n_layer > 1024 || k->n_kv_head < 1 || k->n_kv_head > 1024) return false;
-  if (k->head_dim != 64 && k->head_dim != 128) return false;
-  if (k->page_size != 16 && k->page_size != 32 && k->page_size != 64 && k->page_size != 128) return false;
-  if (k->num_pages < 1 || k->num_pages > kv8::MAX_PAGES || k->num_slots < 1 || k->num_slots > kv8::MAX_SLOTS) return false;
-  if (k->max_pages < 1 || (long)k->max_pages * k->page_size > kv8::MAX_TOKENS) return false;
-  if (!aligned16(k->d_codes) || !aligned16(k->d_refs)) return false;
-  c.fmt = k->format;
-  c.L = k->n_layer;
-  c.kvh = k->n_kv_head;
-  c.d = k->head_dim;
-  c.ps = k->page_size;
-  c.ps_log2 = k->page_size == 16 ? 4 : k->page_size == 32 ? 5 : k->page_size == 64 ? 6 : 7;
-  c.num_pages = k->num_pages;
-  c.num_slots = k->num_slots;
-  c.max_pages = k->max_pages;
-  c.codes = (uint8_t*)k->d_codes;
-  c.scales = k->d_scales;
-  c.table = k->d_table;
-  c.lens = k->d_lens;
-  c.refs = k->d_refs;
-  return true;
-}
-
 static bool kv8_work_ok(const kv8::Cache& c, int n, const void* work, size_t bytes) {
   return work && aligned16(work) && bytes >= kv8::workspace_bytes(n, c.num_pages);
 }
@@ -441,14 +415,14 @@ static bool kv8_ptr_ok(const void* p, int64_t ld, long width) {
 
 size_t gpt2_kv8_workspace_bytes(const gpt2_kv8* k, int n) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || n < 0 || n > GPT2_KV8_MAX_SEQS) return 0;
+  if (!kv8::cache_of(k, c) || n < 0 || n > GPT2_KV8_MAX_SEQS) return 0;
   return kv8::workspace_bytes(n, c.num_pages);
 }
 
 int gpt2_kv8_resize(const gpt2_kv8* k, const int32_t* slots, const int32_t* new_lens, int n, void* work,
                     size_t work_bytes, void* stream) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || !kv8_counts_ok(n, 0)) return GPT2_EINVAL;
+  if (!kv8::cache_of(k, c) || !kv8_counts_ok(n, 0)) return GPT2_EINVAL;
   if (n == 0) return GPT2_OK;
   if (!slots || !new_lens || !kv8_work_ok(c, n, work, work_bytes)) return GPT2_EINVAL;
   return kv8::resize(c, slots, new_lens, n, work, (cudaStream_t)stream) == cudaSuccess ? GPT2_OK : GPT2_ECUDA;
@@ -457,7 +431,7 @@ int gpt2_kv8_resize(const gpt2_kv8* k, const int32_t* slots, const int32_t* new_
 int gpt2_kv8_fork(const gpt2_kv8* k, const int32_t* src, const int32_t* dst, int n, void* work, size_t work_bytes,
                   void* stream) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || !kv8_counts_ok(n, 0)) return GPT2_EINVAL;
+  if (!kv8::cache_of(k, c) || !kv8_counts_ok(n, 0)) return GPT2_EINVAL;
   if (n == 0) return GPT2_OK;
   if (!src || !dst || !kv8_work_ok(c, n, work, work_bytes)) return GPT2_EINVAL;
   return kv8::fork(c, src, dst, n, work, (cudaStream_t)stream) == cudaSuccess ? GPT2_OK : GPT2_ECUDA;
@@ -465,14 +439,14 @@ int gpt2_kv8_fork(const gpt2_kv8* k, const int32_t* src, const int32_t* dst, int
 
 int gpt2_kv8_compact(const gpt2_kv8* k, int32_t* live, void* work, size_t work_bytes, void* stream) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || !kv8_work_ok(c, 0, work, work_bytes)) return GPT2_EINVAL;
+  if (!kv8::cache_of(k, c) || !kv8_work_ok(c, 0, work, work_bytes)) return GPT2_EINVAL;
   return kv8::compact(c, live, work, (cudaStream_t)stream) == cudaSuccess ? GPT2_OK : GPT2_ECUDA;
 }
 
 int gpt2_kv8_append(const gpt2_kv8* k, int layer, const void* d_k, const void* d_v, int64_t ld, const int32_t* slots,
                     const int32_t* cu, int n, int rows, void* stream) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || layer < 0 || layer >= c.L || !kv8_counts_ok(n, rows)) return GPT2_EINVAL;
+  if (!kv8::cache_of(k, c) || layer < 0 || layer >= c.L || !kv8_counts_ok(n, rows)) return GPT2_EINVAL;
   if (n == 0 || rows == 0) return GPT2_OK;
   if (!slots || !cu || !kv8_ptr_ok(d_k, ld, (long)c.kvh * c.d) || !kv8_ptr_ok(d_v, ld, (long)c.kvh * c.d))
     return GPT2_EINVAL;
@@ -488,7 +462,7 @@ static bool kv8_heads_ok(const kv8::Cache& c, int n_head) {
 
 size_t gpt2_kv8_attention_workspace_bytes(const gpt2_kv8* k, int n_head, int n, int rows, int max_q) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || !kv8_heads_ok(c, n_head) || n < 0 || n > GPT2_KV8_MAX_SEQS || rows < 0 || max_q < 1) return 0;
+  if (!kv8::cache_of(k, c) || !kv8_heads_ok(c, n_head) || n < 0 || n > GPT2_KV8_MAX_SEQS || rows < 0 || max_q < 1) return 0;
   return kv8::attention_workspace_bytes(c, n_head, n, rows, max_q);
 }
 
@@ -496,7 +470,7 @@ int gpt2_kv8_attention(const gpt2_kv8* k, int layer, const void* q, int64_t ldq,
                        int n_head, const int32_t* slots, const int32_t* cu, int n, int rows, int max_q, void* work,
                        size_t work_bytes, void* stream) {
   kv8::Cache c;
-  if (!kv8_cache(k, c) || layer < 0 || layer >= c.L || !kv8_heads_ok(c, n_head) || max_q < 1 || !kv8_counts_ok(n, rows))
+  if (!kv8::cache_of(k, c) || layer < 0 || layer >= c.L || !kv8_heads_ok(c, n_head) || max_q < 1 || !kv8_counts_ok(n, rows))
     return GPT2_EINVAL;
   if (n == 0 || rows == 0) return GPT2_OK;
   if (!slots || !cu || !kv8_ptr_ok(q, ldq, (long)n_head * c.d) || !kv8_ptr_ok(out, ldo, (long)n_head * c.d))
@@ -547,11 +521,23 @@ int gpt2_decode_step(gpt2_t* h, const int32_t* d_tokens, int B, int pos, float t
   return decode_impl(h, d_tokens, B, pos, temperature, top_k, seed, d_next);
 }
 
+int gpt2_kv8_prefill(gpt2_t* h, const gpt2_kv8* cache, const int32_t* d_slots, const int32_t* d_tokens, int B, int T0,
+                     float temperature, int top_k, uint64_t seed, int32_t* d_next) {
+  if (h == nullptr) return GPT2_EINVAL;
+  return paged_prefill_impl(h, cache, d_slots, d_tokens, B, T0, temperature, top_k, seed, d_next);
+}
+
+int gpt2_kv8_decode_step(gpt2_t* h, const gpt2_kv8* cache, const int32_t* d_slots, const int32_t* d_tokens, int B,
+                         float temperature, int top_k, uint64_t seed, int32_t* d_next) {
+  if (h == nullptr) return GPT2_EINVAL;
+  return paged_decode_impl(h, cache, d_slots, d_tokens, B, temperature, top_k, seed, d_next);
+}
+
 int gpt2_get_decode_logits(gpt2_t* h, float* dst) {
   if (h == nullptr || dst == nullptr) return GPT2_EINVAL;
-  if (h->gen_B == 0) return set_err(h, GPT2_ESTATE, "no prefill yet");
+  if (h->dec_rows == 0) return set_err(h, GPT2_ESTATE, "no prefill yet");
   RET_IF(check_device_flags(h));
-  const size_t n = (size_t)h->gen_B * h->Vp;
+  const size_t n = (size_t)h->dec_rows * h->Vp;
   std::vector<uint16_t> tmp(n);
   CU_CHECK(h, cudaMemcpy(tmp.data(), h->dec_logits, n * 2, cudaMemcpyDeviceToHost));
   for (size_t i = 0; i < n; ++i) {

@@ -114,6 +114,12 @@ struct gpt2 {
   bf16 *dec_ln = nullptr, *dec_qkv = nullptr, *dec_att = nullptr, *dec_u = nullptr, *dec_a = nullptr;
   bf16* dec_logits = nullptr;  // [max_B, Vp] logits of the last prefill / decode step
   int gen_B = 0, gen_len = 0;  // sequences and positions held in the cache
+  int dec_rows = 0;            // rows of dec_logits
+  // generation on the caller's paged 8-bit cache: per-row positions, new
+  // lengths and row offsets of a call, and the cache calls' scratch
+  int32_t *pg_pos = nullptr, *pg_len = nullptr, *pg_cu = nullptr;
+  uint8_t* pg_work = nullptr;
+  size_t pg_work_bytes = 0;
   const int32_t* last_tok = nullptr;
   const int32_t* last_tgt = nullptr;
 
@@ -251,7 +257,7 @@ static void free_all(gpt2* h) {
                   h->psum_buf, h->dres_bf,  h->dbig,     h->dqkv,     h->datt,     h->slot_buf,
                   h->emb_keys, h->emb_part, h->normbuf, h->d_step, h->norm_part, h->segs,    h->d_bad,    h->tok_dev,
                   h->tgt_dev, h->ce_part, h->attn_ds, h->kv, h->dec_x, h->dec_mean, h->dec_rstd, h->dec_ln,
-                  h->dec_qkv, h->dec_att, h->dec_u, h->dec_a, h->dec_logits};
+                  h->dec_qkv, h->dec_att, h->dec_u, h->dec_a, h->dec_logits, h->pg_pos, h->pg_len, h->pg_cu, h->pg_work};
   for (void* p : ptrs)
     if (p) cudaFree(p);
 }

@@ -14,7 +14,13 @@
 // temperature 0 is the greedy argmax.  The uniform u of row b for the token at
 // position p is the top 53 bits of splitmix64(seed * 2^32 + p * 2^16 + b)
 // (Steele, Lea and Flood's generator), so a CPU restatement draws the same u.
+//
+// The same on a paged 8-bit cache that the caller owns (gpt2_kv8_prefill,
+// gpt2_kv8_decode_step): sequences of different lengths, each row at its own
+// slot's next position; keys and values are rounded into the cache and the
+// attention reads it.
 #pragma once
+#include "kv8_prompt.cuh"
 #include "model_pass.cuh"
 
 namespace gen {
@@ -22,16 +28,16 @@ namespace gen {
 constexpr int SAMPLE_THREADS = 1024;
 constexpr int MAX_TOP_K = 64;
 
-// x[b] = wte[tok[b]] + wpe[pos] (fp32); ids outside [0, Vp) flag the error
+// x[b] = wte[tok[b]] + wpe[pos] (fp32), pos_of[b] instead of pos where given; ids outside [0, Vp) flag the error
 // word and embed as wpe only
 __global__ void embed_kernel(const int32_t* __restrict__ tok, const float* __restrict__ wte,
                              const float* __restrict__ wpe, float* __restrict__ x, int B, int C, int Vp, int pos,
-                             int* __restrict__ bad) {
+                             const int32_t* __restrict__ pos_of, int* __restrict__ bad) {
   const int c4 = C / 4;
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < B * c4; i += gridDim.x * blockDim.x) {
     const int b = i / c4, c = i % c4;
     const int id = tok[b];
-    float4 p = reinterpret_cast<const float4*>(wpe + (long)pos * C)[c];
+    float4 p = reinterpret_cast<const float4*>(wpe + (long)(pos_of ? pos_of[b] : pos) * C)[c];
     if (id >= 0 && id < Vp) {
       const float4 w = reinterpret_cast<const float4*>(wte + (long)id * C)[c];
       p.x += w.x;
@@ -150,10 +156,14 @@ __device__ __forceinline__ bool before(float v, int i, float w, int j) { return 
 // One CTA per sequence: the next token from its logits row z (bf16 [Vp],
 // row stride ld) over ids [0, V).  k rounds each find the next element in
 // (logit desc, id asc) order; p_i = exp((z_i - z_top) / temperature) in
-// double, inverse CDF at u.  top_k <= 1 or temperature <= 0: argmax.
+// double, inverse CDF at u.  top_k <= 1 or temperature <= 0: argmax.  The
+// draw's position and sequence are pos_next and the row, or pos_of[row] + 1 and
+// seq_of[row] where given.
 __global__ void __launch_bounds__(SAMPLE_THREADS) sample_kernel(const bf16* __restrict__ z, long ld, int V,
                                                                float temperature, int top_k, uint64_t seed,
-                                                               int pos_next, int32_t* __restrict__ next) {
+                                                               int pos_next, const int32_t* __restrict__ pos_of,
+                                                               const int32_t* __restrict__ seq_of,
+                                                               int32_t* __restrict__ next) {
   __shared__ float bv[SAMPLE_THREADS / 32];
   __shared__ int bi[SAMPLE_THREADS / 32];
   __shared__ float top_v[MAX_TOP_K];
@@ -210,7 +220,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS) sample_kernel(const bf16* __re
         p[r] = exp(((double)top_v[r] - (double)top_v[0]) / (double)temperature);
         tot += p[r];
       }
-      const uint64_t key = ((seed & 0xFFFFFFFFull) << 32) | ((uint64_t)(pos_next & 0xFFFF) << 16) | (uint64_t)(b & 0xFFFF);
+      const int p_next = pos_of ? pos_of[b] + 1 : pos_next, seq = seq_of ? seq_of[b] : b;
+      const uint64_t key = ((seed & 0xFFFFFFFFull) << 32) | ((uint64_t)(p_next & 0xFFFF) << 16) | (uint64_t)(seq & 0xFFFF);
       const double u = (double)(sm64(key) >> 11) * (1.0 / 9007199254740992.0);
       double c = 0.0;
       pick = top_i[k - 1];
@@ -226,21 +237,55 @@ __global__ void __launch_bounds__(SAMPLE_THREADS) sample_kernel(const bf16* __re
   }
 }
 
+// Before a paged step's resize: row b's token goes to the slot's position
+// lens[slot], or, for a prefill, T0 tokens to 0 .. T0 - 1.  A slot out of range
+// or without room (P positions) asks for the length -1, which refuses the call.
+__global__ void paged_before_kernel(const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int num_slots,
+                                    int P, int B, int T0, int32_t* __restrict__ pos, int32_t* __restrict__ new_len) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= B) return;
+  const int slot = slots[b];
+  const int len = T0 > 0 ? 0 : (unsigned)slot < (unsigned)num_slots ? lens[slot] : P;
+  const int after = len + (T0 > 0 ? T0 : 1);
+  pos[b] = after <= P ? after - 1 : 0;
+  new_len[b] = after <= P ? after : -1;
+}
+// After it: the row offsets of append and attention, all 0 (no rows) when the
+// resize was refused, so that the cache stays as it was.
+__global__ void paged_after_kernel(const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int num_slots,
+                                   int B, int rows, const int32_t* __restrict__ new_len, int32_t* __restrict__ cu) {
+  bool ok = true;
+  for (int b = threadIdx.x; b < B; b += blockDim.x)
+    ok &= (unsigned)slots[b] < (unsigned)num_slots && lens[slots[b]] == new_len[b];
+  ok = __syncthreads_and(ok);
+  for (int b = threadIdx.x; b <= B; b += blockDim.x) cu[b] = ok ? b * rows : 0;
+}
+
 }  // namespace gen
 
 static int gen_alloc(gpt2* h) {
-  if (h->kv != nullptr) return GPT2_OK;
   const long mb = h->maxB, C = h->C;
-  ALLOC(h, h->kv, (size_t)h->L * mb * h->P * 2 * C * 2);
-  ALLOC(h, h->dec_x, (size_t)mb * C * 4);
-  ALLOC(h, h->dec_mean, (size_t)mb * 4);
-  ALLOC(h, h->dec_rstd, (size_t)mb * 4);
-  ALLOC(h, h->dec_ln, (size_t)mb * C * 2);
-  ALLOC(h, h->dec_qkv, (size_t)mb * 3 * C * 2);
-  ALLOC(h, h->dec_att, (size_t)mb * C * 2);
-  ALLOC(h, h->dec_u, (size_t)mb * 4 * C * 2);
-  ALLOC(h, h->dec_a, (size_t)mb * 4 * C * 2);
-  ALLOC(h, h->dec_logits, (size_t)mb * h->Vp * 2);
+  if (h->dec_logits != nullptr) return GPT2_OK;
+#define GEN_ALLOC(ptr, bytes) \
+  if ((ptr) == nullptr) ALLOC(h, ptr, bytes)
+  GEN_ALLOC(h->dec_x, (size_t)mb * C * 4);
+  GEN_ALLOC(h->dec_mean, (size_t)mb * 4);
+  GEN_ALLOC(h->dec_rstd, (size_t)mb * 4);
+  GEN_ALLOC(h->dec_ln, (size_t)mb * C * 2);
+  GEN_ALLOC(h->dec_qkv, (size_t)mb * 3 * C * 2);
+  GEN_ALLOC(h->dec_att, (size_t)mb * C * 2);
+  GEN_ALLOC(h->dec_u, (size_t)mb * 4 * C * 2);
+  GEN_ALLOC(h->dec_a, (size_t)mb * 4 * C * 2);
+  GEN_ALLOC(h->pg_pos, (size_t)mb * 4);
+  GEN_ALLOC(h->pg_len, (size_t)mb * 4);
+  GEN_ALLOC(h->pg_cu, (size_t)(mb + 1) * 4);
+  GEN_ALLOC(h->dec_logits, (size_t)mb * h->Vp * 2);
+#undef GEN_ALLOC
+  return GPT2_OK;
+}
+// the dense cache of gpt2_prefill / gpt2_decode_step
+static int gen_alloc_dense(gpt2* h) {
+  if (h->kv == nullptr) ALLOC(h, h->kv, (size_t)h->L * h->maxB * h->P * 2 * h->C * 2);
   return GPT2_OK;
 }
 
@@ -253,10 +298,18 @@ static int gen_check(gpt2* h, float temperature, int top_k, int32_t* d_next) {
 }
 
 static int gen_sample(gpt2* h, const bf16* rows, long ld, int B, float temperature, int top_k, uint64_t seed,
-                      int pos_next, int32_t* d_next) {
+                      int pos_next, const int32_t* pos_of, const int32_t* seq_of, int32_t* d_next) {
   gen::sample_kernel<<<B, gen::SAMPLE_THREADS, 0, h->stream>>>(rows, ld, h->V, temperature, top_k, seed, pos_next,
-                                                              d_next);
+                                                              pos_of, seq_of, d_next);
   LAUNCH_CHECK(h);
+  h->dec_rows = B;
+  return GPT2_OK;
+}
+
+// the last position's logits of every sequence: rows b*T0 + T0-1
+static int gen_last_logits(gpt2* h, int B, int T0) {
+  CU_CHECK(h, cudaMemcpy2DAsync(h->dec_logits, (size_t)h->Vp * 2, (const bf16*)h->logits + (size_t)(T0 - 1) * h->Vp,
+                                (size_t)T0 * h->Vp * 2, (size_t)h->Vp * 2, B, cudaMemcpyDeviceToDevice, h->stream));
   return GPT2_OK;
 }
 
@@ -266,6 +319,7 @@ static int prefill_impl(gpt2* h, const int32_t* tok, int B, int T0, float temper
                         int32_t* d_next) {
   RET_IF(gen_check(h, temperature, top_k, d_next));
   if (T0 > h->P) return set_err(h, GPT2_EINVAL, "prefix longer than block_size");
+  RET_IF(gen_alloc_dense(h));
   RET_IF(forward_impl(h, tok, nullptr, B, T0, false, 1.f));
   const int C = h->C;
   Views w{h};
@@ -275,13 +329,30 @@ static int prefill_impl(gpt2* h, const int32_t* tok, int B, int T0, float temper
         (const bf16*)w.qkv(l), h->kv + (size_t)l * h->maxB * h->P * 2 * C, B, T0, C, h->P);
     LAUNCH_CHECK(h);
   }
-  // the last position's logits of every sequence: rows b*T0 + T0-1
-  CU_CHECK(h, cudaMemcpy2DAsync(h->dec_logits, (size_t)h->Vp * 2, (const bf16*)h->logits + (size_t)(T0 - 1) * h->Vp,
-                                (size_t)T0 * h->Vp * 2, (size_t)h->Vp * 2, B, cudaMemcpyDeviceToDevice, h->stream));
-  RET_IF(gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, T0, d_next));
+  RET_IF(gen_last_logits(h, B, T0));
+  RET_IF(gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, T0, nullptr, nullptr, d_next));
   h->gen_B = B;
   h->gen_len = T0;
   return GPT2_OK;
+}
+
+// The layers of one decode step on the rows of dec_x [B, C], and the logits;
+// attend(layer) turns dec_qkv into dec_att.
+template <class Attend>
+static int decode_layers(gpt2* h, int B, Attend attend) {
+  const int C = h->C, L = h->L;
+  for (int l = 0; l < L; ++l) {
+    const LayerOffsets& o = h->lo[l];
+    RET_IF(op_ln_fwd(h, h->dec_x, o.ln1g, o.ln1b, h->dec_ln, h->dec_mean, h->dec_rstd, B));
+    RET_IF(op_lin_fwd(h, h->dec_ln, B, C, o.attnw, 3 * C, o.attnb, LIN_PLAIN, h->dec_qkv, nullptr, nullptr));
+    RET_IF(attend(l));
+    RET_IF(op_lin_fwd(h, h->dec_att, B, C, o.projw, C, o.projb, LIN_RESID, h->dec_x, nullptr, h->dec_x));
+    RET_IF(op_ln_fwd(h, h->dec_x, o.ln2g, o.ln2b, h->dec_ln, h->dec_mean, h->dec_rstd, B));
+    RET_IF(op_lin_fwd(h, h->dec_ln, B, C, o.fcw, 4 * C, o.fcb, LIN_GELU, h->dec_u, h->dec_a, nullptr));
+    RET_IF(op_lin_fwd(h, h->dec_a, B, 4 * C, o.mpw, C, o.mpb, LIN_RESID, h->dec_x, nullptr, h->dec_x));
+  }
+  RET_IF(op_ln_fwd(h, h->dec_x, h->lnfg, h->lnfb, h->dec_ln, h->dec_mean, h->dec_rstd, B));
+  return op_lin_fwd(h, h->dec_ln, B, C, h->wte, h->Vp, NO_OFF, LIN_NOBIAS, h->dec_logits, nullptr, nullptr);
 }
 
 // One decode step: tokens [B] at position pos (= the number of positions the
@@ -293,32 +364,106 @@ static int decode_impl(gpt2* h, const int32_t* tok, int B, int pos, float temper
   if (B != h->gen_B || B < 1) return set_err(h, GPT2_ESTATE, "decode needs a prefill with the same batch first");
   if (pos != h->gen_len) return set_err(h, GPT2_ESTATE, "decode position must follow the cached positions");
   if (pos >= h->P) return set_err(h, GPT2_EINVAL, "position reaches block_size");
-  const int C = h->C, L = h->L;
+  const int C = h->C;
   {
     KTimer kt(h, KC_EMB, 0.0, 8.0 * B * C);
-    gen::embed_kernel<<<grid_for((long)B * C / 4, 256), 256, 0, h->stream>>>(tok, h->P32(h->wte), h->P32(h->wpe),
-                                                                             h->dec_x, B, C, h->Vp, pos, h->d_bad);
+    gen::embed_kernel<<<grid_for((long)B * C / 4, 256), 256, 0, h->stream>>>(
+        tok, h->P32(h->wte), h->P32(h->wpe), h->dec_x, B, C, h->Vp, pos, nullptr, h->d_bad);
     LAUNCH_CHECK(h);
   }
   const float sl2 = 1.4426950408889634f / sqrtf((float)(C / h->H));
-  for (int l = 0; l < L; ++l) {
-    const LayerOffsets& o = h->lo[l];
-    RET_IF(op_ln_fwd(h, h->dec_x, o.ln1g, o.ln1b, h->dec_ln, h->dec_mean, h->dec_rstd, B));
-    RET_IF(op_lin_fwd(h, h->dec_ln, B, C, o.attnw, 3 * C, o.attnb, LIN_PLAIN, h->dec_qkv, nullptr, nullptr));
-    {
-      KTimer kt(h, KC_ATTN_F, 4.0 * B * (pos + 1.0) * C, 0.0);
-      gen::attn_kernel<<<B * h->H, 256, (size_t)(pos + 1) * 4, h->stream>>>(
-          h->dec_qkv, h->kv + (size_t)l * h->maxB * h->P * 2 * C, h->dec_att, h->H, h->P, pos, sl2);
-      LAUNCH_CHECK(h);
-    }
-    RET_IF(op_lin_fwd(h, h->dec_att, B, C, o.projw, C, o.projb, LIN_RESID, h->dec_x, nullptr, h->dec_x));
-    RET_IF(op_ln_fwd(h, h->dec_x, o.ln2g, o.ln2b, h->dec_ln, h->dec_mean, h->dec_rstd, B));
-    RET_IF(op_lin_fwd(h, h->dec_ln, B, C, o.fcw, 4 * C, o.fcb, LIN_GELU, h->dec_u, h->dec_a, nullptr));
-    RET_IF(op_lin_fwd(h, h->dec_a, B, 4 * C, o.mpw, C, o.mpb, LIN_RESID, h->dec_x, nullptr, h->dec_x));
-  }
-  RET_IF(op_ln_fwd(h, h->dec_x, h->lnfg, h->lnfb, h->dec_ln, h->dec_mean, h->dec_rstd, B));
-  RET_IF(op_lin_fwd(h, h->dec_ln, B, C, h->wte, h->Vp, NO_OFF, LIN_NOBIAS, h->dec_logits, nullptr, nullptr));
-  RET_IF(gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, pos + 1, d_next));
+  RET_IF(decode_layers(h, B, [&](int l) -> int {
+    KTimer kt(h, KC_ATTN_F, 4.0 * B * (pos + 1.0) * C, 0.0);
+    gen::attn_kernel<<<B * h->H, 256, (size_t)(pos + 1) * 4, h->stream>>>(
+        h->dec_qkv, h->kv + (size_t)l * h->maxB * h->P * 2 * C, h->dec_att, h->H, h->P, pos, sl2);
+    LAUNCH_CHECK(h);
+    return GPT2_OK;
+  }));
+  RET_IF(gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, pos + 1, nullptr, nullptr, d_next));
   h->gen_len = pos + 1;
   return GPT2_OK;
+}
+
+// ------------------------------------------------ on a paged 8-bit cache
+// Checks of both calls, and scratch for `max_q` new tokens of B sequences.
+static int paged_check(gpt2* h, const gpt2_kv8* cache, kv8::Cache& c, const int32_t* slots, const int32_t* tok, int B,
+                       float temperature, int top_k, int32_t* d_next) {
+  RET_IF(gen_check(h, temperature, top_k, d_next));
+  if (slots == nullptr || tok == nullptr) return set_err(h, GPT2_EINVAL, "slots or tokens pointer is NULL");
+  if (B < 1 || B > h->maxB) return set_err(h, GPT2_EINVAL, "B out of range");
+  if (!kv8::cache_of(cache, c)) return set_err(h, GPT2_EINVAL, "the cache's sizes or pointers are out of their limits");
+  if (c.L != h->L || c.kvh != h->H || c.d != h->C / h->H)
+    return set_err(h, GPT2_EINVAL, "the cache has other layers, heads or head dimension than the model");
+  if (B > kv8::MAX_SEQS) return set_err(h, GPT2_EINVAL, "more rows than a cache call takes");
+  const size_t a = kv8::workspace_bytes(B, c.num_pages), b = kv8::attention_workspace_bytes(c, h->H, B, B, 1);
+  const size_t need = a > b ? a : b;
+  if (need > h->pg_work_bytes) {
+    CU_CHECK(h, cudaStreamSynchronize(h->stream));
+    for (size_t i = 0; h->pg_work && i < h->guards.size(); ++i)
+      if (h->guards[i].first == h->pg_work) h->guards.erase(h->guards.begin() + i);
+    if (h->pg_work) cudaFree(h->pg_work);
+    h->pg_work = nullptr;
+    h->pg_work_bytes = 0;
+    ALLOC(h, h->pg_work, need);
+    h->pg_work_bytes = need;
+  }
+  return GPT2_OK;
+}
+
+// The slots' lengths for T0 new tokens from position 0 (T0 > 0) or one more,
+// and the row offsets (none when refused).
+static int paged_room(gpt2* h, const kv8::Cache& c, const int32_t* slots, int B, int T0) {
+  gen::paged_before_kernel<<<(B + 255) / 256, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, h->P, B, T0, h->pg_pos,
+                                                                  h->pg_len);
+  LAUNCH_CHECK(h);
+  CU_CHECK(h, kv8::resize(c, slots, h->pg_len, B, h->pg_work, h->stream));
+  h->launches += 2;
+  gen::paged_after_kernel<<<1, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, B, T0 > 0 ? T0 : 1, h->pg_len, h->pg_cu);
+  LAUNCH_CHECK(h);
+  return GPT2_OK;
+}
+
+static int paged_prefill_impl(gpt2* h, const gpt2_kv8* cache, const int32_t* slots, const int32_t* tok, int B, int T0,
+                              float temperature, int top_k, uint64_t seed, int32_t* d_next) {
+  kv8::Cache c;
+  RET_IF(paged_check(h, cache, c, slots, tok, B, temperature, top_k, d_next));
+  if (T0 > h->P) return set_err(h, GPT2_EINVAL, "prefix longer than block_size");
+  RET_IF(forward_impl(h, tok, nullptr, B, T0, false, 1.f));
+  // free the slots, then take T0 tokens each
+  CU_CHECK(h, cudaMemsetAsync(h->pg_len, 0, (size_t)B * 4, h->stream));
+  CU_CHECK(h, kv8::resize(c, slots, h->pg_len, B, h->pg_work, h->stream));
+  h->launches += 2;
+  RET_IF(paged_room(h, c, slots, B, T0));
+  Views w{h};
+  const int C = h->C;
+  for (int l = 0; l < h->L; ++l) {
+    const bf16* qkv = (const bf16*)w.qkv(l);
+    CU_CHECK(h, kv8::append(c, l, qkv + C, qkv + 2 * C, 3L * C, slots, h->pg_cu, B, B * T0, h->stream));
+    h->launches++;
+  }
+  RET_IF(gen_last_logits(h, B, T0));
+  return gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, T0, h->pg_pos, slots, d_next);
+}
+
+static int paged_decode_impl(gpt2* h, const gpt2_kv8* cache, const int32_t* slots, const int32_t* tok, int B,
+                             float temperature, int top_k, uint64_t seed, int32_t* d_next) {
+  kv8::Cache c;
+  RET_IF(paged_check(h, cache, c, slots, tok, B, temperature, top_k, d_next));
+  const int C = h->C;
+  RET_IF(paged_room(h, c, slots, B, 0));
+  {
+    KTimer kt(h, KC_EMB, 0.0, 8.0 * B * C);
+    gen::embed_kernel<<<grid_for((long)B * C / 4, 256), 256, 0, h->stream>>>(
+        tok, h->P32(h->wte), h->P32(h->wpe), h->dec_x, B, C, h->Vp, 0, h->pg_pos, h->d_bad);
+    LAUNCH_CHECK(h);
+  }
+  RET_IF(decode_layers(h, B, [&](int l) -> int {
+    KTimer kt(h, KC_ATTN_F, 0.0, 0.0);  // (the lengths are on the device)
+    CU_CHECK(h, kv8::append(c, l, h->dec_qkv + C, h->dec_qkv + 2 * C, 3L * C, slots, h->pg_cu, B, B, h->stream));
+    CU_CHECK(h, kv8::attention(c, l, h->dec_qkv, 3L * C, h->dec_att, C, nullptr, h->H, slots, h->pg_cu, B, B, 1, h->pg_work,
+                               h->stream));
+    h->launches += 3;
+    return GPT2_OK;
+  }));
+  return gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, 0, h->pg_pos, slots, d_next);
 }

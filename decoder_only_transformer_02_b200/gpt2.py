@@ -15,6 +15,7 @@ import numpy as np
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgpt2.so")
 _lib = None
+_one_device = None
 
 GPT2_FP32 = 0
 GPT2_BF16 = 1
@@ -32,6 +33,7 @@ EXPORTED = [
     "gpt2_prefill", "gpt2_decode_step", "gpt2_get_decode_logits", "gpt2_check_guards",
     "gpt2_debug_overwrite_guard", "gpt2_kv8_workspace_bytes", "gpt2_kv8_resize", "gpt2_kv8_fork",
     "gpt2_kv8_compact", "gpt2_kv8_append", "gpt2_kv8_attention_workspace_bytes", "gpt2_kv8_attention",
+    "gpt2_kv8_prefill", "gpt2_kv8_decode_step",
 ]
 GPT2_KV_INT8 = 0
 GPT2_KV_E4M3 = 1
@@ -118,6 +120,8 @@ def load_library():
         "gpt2_kv8_compact": (I, [P, P, P, S, P]),
         "gpt2_kv8_append": (I, [P, I, P, P, L, P, P, I, I, P]),
         "gpt2_kv8_attention_workspace_bytes": (S, [P, I, I, I, I]),
+        "gpt2_kv8_prefill": (I, [P, P, P, P, I, I, F, I, ctypes.c_uint64, P]),
+        "gpt2_kv8_decode_step": (I, [P, P, P, P, I, F, I, ctypes.c_uint64, P]),
         "gpt2_kv8_attention": (I, [P, I, P, L, P, L, P, I, P, P, I, I, I, P, S, P]),
     }
     for name, (res, args) in sig.items():
@@ -253,6 +257,21 @@ class GPT2:
         B = tokens.shape[0]
         self._check(self._lib.gpt2_decode_step(self._h, _ptr(tokens), B, pos, temperature, top_k, seed,
                                                _ptr(next_out)))
+
+    def kv8_prefill(self, cache, slots, tokens, next_out, temperature=1.0, top_k=1, seed=0):
+        """prefill into a KV8Cache: tokens device int32 [B, T0], the prefixes of
+        the slots (device int32 [B]), which are freed first; next_out: device
+        int32 [B]."""
+        B, T0 = tokens.shape
+        self._check(self._lib.gpt2_kv8_prefill(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, T0, temperature,
+                                               top_k, seed, _ptr(next_out)))
+
+    def kv8_decode_step(self, cache, slots, tokens, next_out, temperature=1.0, top_k=1, seed=0):
+        """One token per slot of a KV8Cache, each at its slot's next position:
+        slots, tokens, next_out device int32 [B]."""
+        B = tokens.shape[0]
+        self._check(self._lib.gpt2_kv8_decode_step(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, temperature,
+                                                   top_k, seed, _ptr(next_out)))
 
     def get_decode_logits(self, B) -> np.ndarray:
         a = np.empty((B, self.cfg.padded_vocab), dtype=np.float32)
@@ -406,7 +425,10 @@ class KV8Cache:
         import torch
         fmts = {torch.int8: GPT2_KV_INT8, torch.float8_e4m3fn: GPT2_KV_E4M3}
         self._torch, self._i32, self._f32, self._bf16 = torch, torch.int32, torch.float32, torch.bfloat16
-        self._only_device = torch.cuda.device_count() == 1
+        global _one_device
+        if _one_device is None:
+            _one_device = torch.cuda.device_count() == 1
+        self._only_device = _one_device
         dev = codes.device
         shapes_ok = codes.dim() == 6 and codes.shape[2] == 2 and codes.dtype in fmts and dev.type == "cuda" and \
             scales.dtype == torch.float32 and tuple(scales.shape) == tuple(codes.shape[:4]) and \
@@ -439,6 +461,11 @@ class KV8Cache:
                    torch.full((num_slots, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(num_slots, dtype=torch.int32, device=device),
                    torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+    @property
+    def handle(self) -> int:
+        """Address of the gpt2_kv8 description."""
+        return self._p
 
     def workspace_bytes(self, n) -> int:
         """Bytes of `work` for resize, fork (up to n entries) and compact."""

@@ -338,6 +338,28 @@ int gpt2_kv8_attention(const gpt2_kv8* cache, int layer, const void* d_q, int64_
                        float* d_lse, int n_head, const int32_t* d_slots, const int32_t* d_cu, int n, int rows,
                        int max_q, void* d_work, size_t work_bytes, void* cuda_stream);
 
+/* ---- generation on a paged 8-bit cache (bf16 mode) ----
+ * gpt2_prefill and gpt2_decode_step (above) with the caller's gpt2_kv8 in place
+ * of the handle's own cache: sequences of different lengths, which can be
+ * forked, cut back and freed between the calls with gpt2_kv8_fork and
+ * gpt2_kv8_resize.  The cache has the model's layers, n_kv_head = n_head and
+ * head_dim 64.  Row b of a call works on slot d_slots[b] (device int32 [B],
+ * distinct); the draw for its token at position p uses the slot in the place
+ * of the sequence's number: splitmix64(seed * 2^32 + p * 2^16 + slot).  The
+ * first call allocates the step's buffers.  A call that the cache refuses
+ * (GPT2_ECACHE at the next syncing call) leaves the cache as it was, except
+ * that a refused prefill has freed its slots; d_next is then meaningless.
+ * Prefill: the slots are freed and hold positions 0 .. T0-1 of d_tokens
+ * [B, T0] (T0 <= max_T) afterwards; the prefix itself attends to its unrounded
+ * keys and values. */
+int gpt2_kv8_prefill(gpt2_t* h, const gpt2_kv8* cache, const int32_t* d_slots, const int32_t* d_tokens, int B, int T0,
+                     float temperature, int top_k, uint64_t seed, int32_t* d_next);
+/* One step: d_tokens [B] are the tokens at each slot's next position (its
+ * length, below block_size); appends their keys and values and samples the
+ * tokens that follow. */
+int gpt2_kv8_decode_step(gpt2_t* h, const gpt2_kv8* cache, const int32_t* d_slots, const int32_t* d_tokens, int B,
+                         float temperature, int top_k, uint64_t seed, int32_t* d_next);
+
 /* ---- device-side errors of the standalone operators ----
  * The kernels never trap.  A pipeline wait that gives up (a producer or
  * consumer that did not arrive within the wait limit) records an error code

@@ -10,16 +10,17 @@
 // and the result is O / sum P as in the streaming kernel (kv8_attention.cuh).
 //
 // The tensor cores read f16 from shared memory, the cache holds 8-bit codes, so
-// four warps convert each block on its way: the codes of the next 16 KB are
+// six warps convert each block on its way: the codes of the next 16 KB are
 // loaded while these 16 KB are converted and stored as swizzled f16 tiles.  A
 // key block's values are code * scale / (the block's largest scale), exact in
 // f16 unless 2^15 or more below it; the largest scale multiplies the scores.
 // Values are taken relative to the largest scale so far; when that rises, O is
 // scaled down as it is when the row maximum moves.
 //
-// Roles (512 threads, one CTA per SM, some registers moved to the softmax):
-// warps 0-3 convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warp
-// 12 issues the MMAs of both.  Two tiles per
+// Roles (512 threads of 128 registers, one CTA per SM; registers moved from the
+// converting warps to the softmax cost more there than they gave here):
+// warps 0-3, 14 and 15 convert, warps 4-7 and 8-11 are the softmax of tile 0 and
+// 1, warps 12 and 13 issue their MMAs.  Two tiles per
 // CTA instead of two CTAs of one tile: the conversion is done once for both,
 // and one tile's exponentials run while the other's MMAs do.
 //
@@ -35,11 +36,7 @@
 namespace kv8 {
 
 constexpr int W_THREADS = 512;
-constexpr int W_CONV = 4;    // converting warps
-// Registers of a thread: the launch gives every warp W_REGS; the warpgroups
-// (converting, softmax twice, MMA) share them out anew.
-constexpr int W_REGS = 128, W_REGS_CONV = 128, W_REGS_SOFT = 144, W_REGS_MMA = 96;
-static_assert(W_REGS_CONV + 2 * W_REGS_SOFT + W_REGS_MMA <= 4 * W_REGS, "the launch's registers, no more");
+constexpr int W_CONV = 6;    // converting warps
 constexpr int W_ROWS = 256;  // rows of a work item (two tiles)
 constexpr int W_KEYS = 128;  // keys of a block
 
@@ -52,20 +49,11 @@ struct Wide {
   static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale, value scale so far
   static constexpr int LINE_OFF = INFO_OFF + 256;
   static constexpr int UNITS = D / 64;                   // 16 KB units of codes in a block: all of it, or keys, values
-  static constexpr int HALVES = 2 / UNITS;               // sides in a unit
   // TMEM columns of a tile: S, P (in place of S's first 64 when d = 128), O
   static constexpr uint32_t T_P = D == 64 ? 128 : 0, T_O = D == 64 ? 192 : 128;
   static size_t bytes(int n) { return LINE_OFF + (size_t)(n + 1) * 8 + 1024; }
 };
 
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -214,14 +202,14 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);  // NS, count W_CONV
-  uint64_t* kv_empty = kv_full + NS;                                   // NS: both tiles' MMAs have read the stage
+  uint64_t* kv_empty = kv_full + NS;                                   // NS, count 2: the tile's MMAs have read the stage
   uint64_t* q_full = kv_empty + NS;                                    // 2, count 4: the tile's Q is in shared memory
   uint64_t* s_full = q_full + 2;                                       // 2: S in TMEM
   uint64_t* s_free = s_full + 2;                                       // 2, count 4: S is in registers
   uint64_t* p_full = s_free + 2;                                       // 2, count 4: P in TMEM (and O rescaled)
   uint64_t* pv_done = p_full + 2;                                      // 2: O += P V complete
-  uint64_t* drain = pv_done + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = pv_done + 2;                                       // 2
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   float2* info = reinterpret_cast<float2*>(smem + S::INFO_OFF);
   long long* s_warp = reinterpret_cast<long long*>(smem + S::INFO_OFF + 128);
   long long* pre = reinterpret_cast<long long*>(smem + S::LINE_OFF);
@@ -232,7 +220,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], W_CONV);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&q_full[a], 4);
@@ -240,8 +228,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       mbar_init(&s_free[a], 4);
       mbar_init(&p_full[a], 4);
       mbar_init(&pv_done[a], 1);
+      mbar_init(&drain[a], 1);
     }
-    mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) {
@@ -259,94 +247,80 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   long long at = blockIdx.x * per;
   const long long end = min(total, at + per);
 
-  if (warp >= 12) {
-    regs_down<W_REGS_MMA>();
-    if (threadIdx.x == 384) {
-        // ---------------------------------------------------- MMA issuer
-        constexpr uint32_t id_s = f16_idesc(W_KEYS, 0), id_pv = f16_idesc(D, 1);
-        uint32_t g = 0, t[2] = {0, 0}, items[2] = {0, 0};
-        bool ok = true;
-        int join_parts = 0;
-        auto do_s = [&](int a, int stage) {
-          const uint32_t qa = smem_u32(smem + a * S::TILE), ka = smem_u32(smem + S::KV_OFF + 2 * stage * S::TILE);
+  if (warp == 12 || warp == 13) {
+    if (lane == 0) {
+      // ---------------------------------------------- MMA issuer of a tile
+      const int a = warp - 12;
+      constexpr uint32_t id_s = f16_idesc(W_KEYS, 0), id_pv = f16_idesc(D, 1);
+      const uint32_t qa = smem_u32(smem + a * S::TILE), ta = tmem + a * 256;
+      uint32_t g = 0, t = 0, items = 0;
+      bool ok = true;
+      int join_parts = 0;
+      auto do_pv = [&](uint32_t gp, bool first) {  // of the tile's latest S, whose block is number gp
+        if (!mbar_wait(&p_full[a], (t - 1) & 1u)) return false;
+        tc_fence_after();
+        const uint32_t va = smem_u32(smem + S::KV_OFF + (2 * (gp % NS) + 1) * S::TILE);
+#pragma unroll
+        for (int kk = 0; kk < W_KEYS / 16; ++kk)
+          tc_mma_ts(ta + S::T_O, ta + S::T_P + kk * 8, v_desc(va + kk * 2048), id_pv, first && kk == 0 ? 0u : 1u);
+        tc_commit(&pv_done[a]);
+        tc_commit(&kv_empty[gp % NS]);
+        return true;
+      };
+      while (ok && at < end) {
+        const Item p = item_at(k, pre, at, end);
+        const int rows = p.q * k.group - p.row0;
+        if (a == 0 && p.b0 == 0 && p.b1 > 0 && p.b1 < p.blocks) {
+          join_parts = (int)((p.next + p.left - 1) / per) - blockIdx.x + 1;
+          Join j;
+          j.parts = join_parts, j.tile_rows = min(W_ROWS, rows), j.row0 = p.row0, j.head = p.head, j.a = p.a;
+          k.join[blockIdx.x] = j;
+        }
+        at = p.next;
+        if (rows <= a * 128) {  // only the other tile has rows: let go of its blocks as they come
+          for (int j = p.b0; ok && j < p.b1; ++j, ++g) {
+            ok = mbar_wait(&kv_full[g % NS], (g / NS) & 1u);
+            if (ok) mbar_arrive(&kv_empty[g % NS]);
+          }
+          continue;
+        }
+        for (int j = p.b0; ok && j < p.b1; ++j, ++g, ++t) {
+          const int s = g % NS;
+          if (j == p.b0) {
+            ok = mbar_wait(&q_full[a], items & 1u);
+            ++items;
+          } else if (D == 64) {
+            ok = mbar_wait(&s_free[a], (t - 1) & 1u);
+          } else {
+            ok = do_pv(g - 1, j - 1 == p.b0);  // P lies in S's place: its product goes first
+          }
+          ok = ok && mbar_wait(&kv_full[s], (g / NS) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ka = smem_u32(smem + S::KV_OFF + 2 * s * S::TILE);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
-            tc_mma(tmem + a * 256, make_sdesc(qa + o, 0), make_sdesc(ka + o, 0), id_s, kk > 0 ? 1u : 0u);
+            tc_mma(ta, make_sdesc(qa + o, 0), make_sdesc(ka + o, 0), id_s, kk > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[a]);
-        };
-        auto do_pv = [&](int a, int stage, bool first) -> bool {  // of the tile's latest S
-          if (!mbar_wait(&p_full[a], (t[a] - 1) & 1u)) return false;
-          tc_fence_after();
-          const uint32_t va = smem_u32(smem + S::KV_OFF + (2 * stage + 1) * S::TILE);
-#pragma unroll
-          for (int kk = 0; kk < W_KEYS / 16; ++kk)
-            tc_mma_ts(tmem + a * 256 + S::T_O, tmem + a * 256 + S::T_P + kk * 8, v_desc(va + kk * 2048), id_pv,
-                      first && kk == 0 ? 0u : 1u);
-          tc_commit(&pv_done[a]);
-          return true;
-        };
-        while (ok && at < end) {
-          const Item p = item_at(k, pre, at, end);
-          const int rows = p.q * k.group - p.row0;
-          if (p.b0 == 0 && p.b1 > 0 && p.b1 < p.blocks) {
-            join_parts = (int)((p.next + p.left - 1) / per) - blockIdx.x + 1;
-            Join j;
-            j.parts = join_parts, j.tile_rows = min(W_ROWS, rows), j.row0 = p.row0, j.head = p.head, j.a = p.a;
-            k.join[blockIdx.x] = j;
-          }
-          at = p.next;
-          const int tiles = rows > 128 ? 2 : 1;
-          for (int j = p.b0; ok && j < p.b1; ++j, ++g) {
-            const int s = g % NS, sp = (g + NS - 1) % NS;
-            if (!mbar_wait(&kv_full[s], (g / NS) & 1u)) {
-              ok = false;
-              break;
-            }
-            for (int a = 0; a < tiles; ++a) {
-              if (j == p.b0) {
-                if (!mbar_wait(&q_full[a], items[a] & 1u)) {
-                  ok = false;
-                  break;
-                }
-                ++items[a];
-              } else if (D == 64) {
-                if (!mbar_wait(&s_free[a], (t[a] - 1) & 1u)) {
-                  ok = false;
-                  break;
-                }
-              } else if (!do_pv(a, sp, j - 1 == p.b0)) {  // P lies in S's place: its product goes first
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              do_s(a, s);
-              if (D == 64 && j > p.b0 && !do_pv(a, sp, j - 1 == p.b0)) {
-                ok = false;
-                break;
-              }
-              ++t[a];
-            }
-            if (ok && j > p.b0) tc_commit(&kv_empty[sp]);
-          }
-          if (ok && p.b1 > p.b0) {
-            const int sp = (g + NS - 1) % NS;
-            for (int a = 0; ok && a < tiles; ++a) ok = do_pv(a, sp, p.b1 - 1 == p.b0);
-            if (ok) tc_commit(&kv_empty[sp]);
-          }
+          if (D == 64 && j > p.b0) ok = do_pv(g - 1, j - 1 == p.b0);
         }
-        if (join_parts == 0) k.join[blockIdx.x].parts = 0;
-        if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
-        tc_commit(drain);
-        if (!mbar_wait_drain(drain, 0)) set_device_err(DERR_WAIT_TIMEOUT);
+        if (ok && p.b1 > p.b0) ok = do_pv(g - 1, p.b1 - 1 == p.b0);
+      }
+      if (a == 0 && join_parts == 0) k.join[blockIdx.x].parts = 0;
+      if (!ok) set_device_err(DERR_WAIT_TIMEOUT);
+      tc_commit(&drain[a]);
+      if (!mbar_wait_drain(&drain[a], 0)) set_device_err(DERR_WAIT_TIMEOUT);
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || warp > 13) {
       // ------------------------------------------------ converting warps
       // A unit is 32 pieces of 512 bytes: 512 / D consecutive tokens' codes, 16
-      // bytes for each lane; warp w takes the pieces w, w + 4, ...
-      constexpr int ROWS = 512 / D, NX = 32 / W_CONV, PARTS = NX / S::HALVES;  // parts of a side that a warp takes in a unit
+      // bytes for each lane; warp w takes the pieces w, w + 6, ...
+      constexpr int ROWS = 512 / D, PER_SIDE = W_KEYS / ROWS, NX = (32 + W_CONV - 1) / W_CONV;
+      const int cw = warp < 4 ? warp : warp - 10;
       const int lrow = lane / (D / 16), lq = lane % (D / 16);
+      auto mine = [&](int e) { return cw + W_CONV * e < 32; };
       uint32_t g = 0;
       bool ok = true;
       const long page_stride = c.page_bytes();
@@ -371,18 +345,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           return table[min(blk * per_block + min(lane, per_block - 1), last_page)];
         };
         auto valid = [&](int page) { return c.page_ok(page) ? page : 0; };
-        uint4 nx[NX];
-        // the warp's pieces of a unit: HALVES sides x PARTS runs of rows
-        auto load = [&](int page, int unit, uint32_t after) {
+        uint4 nx[NX] = {};
+        auto load = [&](int page, int unit, uint32_t after) {  // the warp's pieces of a unit
 #pragma unroll
-          for (int e = 0; e < PARTS; ++e) {
-            const int row0 = (warp + W_CONV * e) * ROWS;
-            const int pg = __shfl_sync(0xffffffffu, page, row0 >> c.ps_log2);
-            const uint8_t* src = head_base + pg * page_stride + ((row0 & (c.ps - 1)) * D + lane * 16 + after);
-#pragma unroll
-            for (int h = 0; h < S::HALVES; ++h)
-              nx[e * S::HALVES + h] = __ldcg(reinterpret_cast<const uint4*>(src + (S::HALVES == 2 ? h : unit) * side_stride));
-          }
+          for (int e = 0; e < NX; ++e)
+            if (mine(e)) {
+              const int i = cw + W_CONV * e + 32 * unit, row0 = (i & (PER_SIDE - 1)) * ROWS;
+              const int pg = __shfl_sync(0xffffffffu, page, row0 >> c.ps_log2);
+              nx[e] = __ldcg(reinterpret_cast<const uint4*>(head_base + pg * page_stride + (i >= PER_SIDE ? side_stride : 0) +
+                                                            ((row0 & (c.ps - 1)) * D + lane * 16 + after)));
+            }
         };
         float vref = 0.f;
         int page = page_id(p.b0), page1 = page_id(p.b0 + 1);
@@ -405,7 +377,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
             ok = false;
             break;
           }
-          if (warp == 0 && lane == 0) info[s] = make_float2(kmax, vref);
+          if (cw == 0 && lane == 0) info[s] = make_float2(kmax, vref);
           const int left = p.len - j * W_KEYS;  // tokens from the block on
 #pragma unroll
           for (int u = 0; u < S::UNITS; ++u) {
@@ -428,25 +400,23 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
               page1 = page_id(j + 2 + after);
             }
 #pragma unroll
-            for (int e = 0; e < PARTS; ++e) {
-              const int row0 = (warp + W_CONV * e) * ROWS, row = row0 + lrow;
-              const uint32_t rows = smem_u32(smem + S::KV_OFF + 2 * s * S::TILE) + (row >> 3) * 1024 + (row & 7) * 128;
-              const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
-#pragma unroll
-              for (int h = 0; h < S::HALVES; ++h) {
-                const int side = S::HALVES == 2 ? h : u;
+            for (int e = 0; e < NX; ++e)
+              if (mine(e)) {
+                const int i = cw + W_CONV * e + 32 * u, side = i >= PER_SIDE;
+                const int row0 = (i & (PER_SIDE - 1)) * ROWS, row = row0 + lrow;
                 const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row0 >> c.ps_log2);
-                uint4 w = cur[e * S::HALVES + h];
+                uint4 w = cur[e];
                 if (left < W_KEYS && row >= left) w = make_uint4(0, 0, 0, 0);
                 uint32_t x[8];
                 codes16_half<FMT>(w, f, x);
                 // the two 16-byte pieces in an order that keeps eight lanes in different banks
                 const bool y = D == 128 && (lq >> 2);
-                const uint32_t tile = rows + side * S::TILE + (D == 128 ? (lq >> 2) * 16384 : 0);
+                const uint32_t tile = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE) + (row >> 3) * 1024 +
+                                      (row & 7) * 128 + (D == 128 ? (lq >> 2) * 16384 : 0);
+                const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
                 sts128(tile + (y ? c0 ^ 16 : c0), y ? x[4] : x[0], y ? x[5] : x[1], y ? x[6] : x[2], y ? x[7] : x[3]);
                 sts128(tile + (y ? c0 : c0 ^ 16), y ? x[0] : x[4], y ? x[1] : x[5], y ? x[2] : x[6], y ? x[3] : x[7]);
               }
-            }
           }
           fence_async_smem();
           __syncwarp();
@@ -456,7 +426,6 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       if (!ok && lane == 0) set_device_err(DERR_WAIT_TIMEOUT);
   } else {
     // -------------------------------------------------- softmax of a tile
-    regs_up<W_REGS_SOFT>();
     const int a = (warp >> 2) - 1, qw = warp & 3, r = qw * 32 + lane;
     const uint32_t tl = tmem + a * 256 + ((uint32_t)(qw * 32) << 16);
     const float sl2 = LOG2E_F * (D == 64 ? 0.125f : 0.08838834764831845f);
@@ -730,11 +699,6 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   using S = Wide<D>;
   static DeviceOnce once;
   cudaError_t e = run_once_per_device(once, [] {
-    // a warp that asks for registers that the launch does not have would wait for good
-    cudaFuncAttributes at;
-    cudaError_t r = cudaFuncGetAttributes(&at, wide_kernel<FMT, D>);
-    if (r != cudaSuccess) return r;
-    if (at.numRegs != W_REGS) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(wide_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes(MAX_SEQS));
   });
   if (e != cudaSuccess) return e;

@@ -559,6 +559,35 @@ def test_offsets_past_32_bits():
     assert torch.all(c.table[3, :3] >= shift)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_wait_that_gives_up_is_reported_and_recovers(d):
+    """The prompt kernel's waits run out at once (none is left hanging); with
+    the limit restored the same call gives the bits it gave before."""
+    p = Pair(R.INT8, kvh=2, d=d, ps=32, num_pages=60, max_pages=40)
+    p.append([0, 1], [900, 500])
+    work = torch.empty(p.dev.attention_workspace_bytes(2, 2, 1000, 700), dtype=torch.uint8, device="cuda")
+    q = torch.randn(1000, 2, d, device="cuda").bfloat16()
+
+    def call():
+        out = torch.zeros_like(q)
+        p.dev.attention(0, q, out, _i32([0, 1]), _i32([0, 700, 1000]), 700, work)
+        return out
+
+    want = call()
+    p.G.check_device_error()
+    try:
+        p.G.set_wait_limit_ns(1)
+        call()
+        with pytest.raises(p.G.GPT2Error) as e:
+            p.G.check_device_error()
+        assert e.value.name == "ECUDA"
+    finally:
+        p.G.set_wait_limit_ns(0)
+    got = call()
+    p.G.check_device_error()
+    assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------- as they are used
 def _step(p, slots, seed, work, awork, news, stream=None):
     """One layerless sampling step: room, append, attention."""

@@ -520,6 +520,10 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     }
     want += total;
   }
+  // a source that is also a destination would be read while it is written
+  __syncthreads();
+  for (int i = tid; i < n && err == 0; i += PLAN_THREADS)
+    if (s_map[src[i] >> 5] >> (src[i] & 31) & 1u) err = DERR_KV8_ARGS;
   bool ok = __syncthreads_or(err) == 0;
   if (ok && find_free(c, want, w.list, s_warp) < want) {
     ok = false;

@@ -261,7 +261,7 @@ size_t gpt2_matmul_workspace_bytes(int M, int N, int K);
  * the next syncing call of a model handle) returns; no kernel traps.  Calls
  * that overlap in time need a workspace each, and must not name the same
  * slots unless both only read (attention); resize, fork and compact change
- * d_refs and must not overlap each other. */
+ * d_refs and must not overlap each other, and compact must not overlap any. */
 #define GPT2_KV_INT8 0 /* signed 8-bit integers, -127..127 */
 #define GPT2_KV_E4M3 1 /* 8-bit floats, 4 exponent and 3 fraction bits, largest 448 */
 #define GPT2_KV8_MAX_SEQS 4096 /* entries of one call */
@@ -296,8 +296,8 @@ int gpt2_kv8_resize(const gpt2_kv8* cache, const int32_t* d_slots, const int32_t
 /* The empty slots d_dst[i] take over the tokens of d_src[i] (which may repeat):
  * full pages are shared, an unfinished last page is copied to a free page
  * (lowest id first, in the order of the list).  Refused as a whole, changing
- * nothing: a slot out of range, a destination that is not empty or named
- * twice, too few free pages. */
+ * nothing: a slot out of range, a destination that is not empty, named twice
+ * or a source too, too few free pages. */
 int gpt2_kv8_fork(const gpt2_kv8* cache, const int32_t* d_src, const int32_t* d_dst, int n, void* d_work,
                   size_t work_bytes, void* cuda_stream);
 /* Move the pages in use to the ids below their number: the j-th used page at
@@ -314,7 +314,8 @@ int gpt2_kv8_compact(const gpt2_kv8* cache, int32_t* d_live, void* d_work, size_
  * The scale of a block is the smallest power of two (at least 2^-126) with
  * which the largest magnitude among its tokens fits the codes' range; when a
  * later token is larger, the block's codes are rounded once more to the grown
- * scale.  Codes are rounded to nearest even.  A value that is not finite makes
+ * scale (and keeps it when that token is cut off again).  Codes are rounded to
+ * nearest even.  A value that is not finite makes
  * its block read as NaN.  A slot named twice (its later entries) or shorter
  * than its rows is skipped and recorded (GPT2_ECACHE); offsets that decrease
  * or pass `rows` refuse the whole call. */

@@ -78,7 +78,7 @@ class Cache:
 
     def fork(self, src, dst):
         slots = list(src) + list(dst)
-        if len(set(dst)) < len(dst) or any(not 0 <= s < self.num_slots for s in slots) or any(self.lens[t] for t in dst):
+        if len(set(dst)) < len(dst) or set(src) & set(dst) or any(not 0 <= s < self.num_slots for s in slots) or any(self.lens[t] for t in dst):
             raise Refused
         free = [p for p in range(self.num_pages) if self.refs[p] == 0]
         if len(free) < sum(self.lens[s] % self.ps > 0 for s in src):

@@ -415,7 +415,8 @@ def test_random_calls(fmt, seed):
                 p.resize(slots, new)
         elif what == 3:
             dst = [int(s) for s in np.flatnonzero(lens == 0)]
-            src = [int(rng.integers(0, 9)) for _ in dst]
+            src = [int(rng.choice(np.flatnonzero(lens > 0))) for _ in dst] if lens.any() else []
+            dst = dst[:len(src)]
             if free >= len(dst):
                 p.fork(src, dst)
         elif what == 4:
@@ -445,7 +446,7 @@ def test_table_calls_refused_as_a_whole():
         p.resize(slots, new, ok=False)
     p.resize([0, 2], [16, 32])       # a page given back serves the same call
     p.resize([2], [0])
-    for src, dst in [([0], [1]), ([0, 1], [3, 3]), ([0], [5]), ([7], [3])]:
+    for src, dst in [([0], [1]), ([0, 1], [3, 3]), ([0], [5]), ([7], [3]), ([0, 3], [3, 4]), ([3], [3]), ([-1], [3])]:
         p.fork(src, dst, ok=False)
     p.fork([0], [3])                 # length 16: nothing to copy
     p.fork([1], [4])
@@ -685,6 +686,36 @@ def test_graph_capture_side_stream_and_determinism():
     for r in runs:
         assert torch.equal(r[2], out4)
         assert torch.equal(r[1].codes.view(torch.uint8), c4.codes.view(torch.uint8))
+
+
+def test_as_many_sequences_as_a_call_takes():
+    """4096 short sequences, and a prompt among them."""
+    G = _g()
+    n = 4096
+    c = G.KV8Cache.allocate(R.E4M3, 1, 1, 64, 16, 5000, n, 300)
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(1)).int().cuda()
+    lens = torch.ones(n, dtype=torch.int32, device="cuda")
+    lens[1234] = 300
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), lens.cumsum(0).int()])
+    rows = int(cu[-1])
+    qkv = torch.randn(rows, 3, 1, 64, device="cuda").bfloat16()
+    work = torch.empty(c.workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    c.resize(slots, lens, work)
+    c.append(0, qkv[:, 1], qkv[:, 2], slots, cu)
+    for max_q in (300, 4096):
+        awork = torch.empty(c.attention_workspace_bytes(1, n, rows, max_q), dtype=torch.uint8, device="cuda")
+        out = torch.zeros(rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+        c.attention(0, qkv[:, 0], out, slots, cu, max_q, awork)
+        G.check_device_error()
+        # a single token's output is its own value as the cache holds it
+        own = torch.ones(rows, dtype=torch.bool, device="cuda")
+        own[1234:1534] = False
+        v = qkv[own, 2, 0].float()
+        assert torch.all((out[own, 0].float() - v).abs() <= 2.0 ** -4 * v.abs() + 2.0 ** -8 * v.abs().amax(-1, keepdim=True))
+        assert torch.isfinite(out).all() and (out[1400:1500].float().std() > 0)
+    with pytest.raises(G.GPT2Error) as e:
+        c.resize(_i32(range(n + 1)), _i32(range(n + 1)), work)
+    assert e.value.name == "EINVAL"
 
 
 def test_empty_calls():

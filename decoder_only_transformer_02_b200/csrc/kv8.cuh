@@ -293,6 +293,9 @@ static inline cudaError_t append(const Cache& c, int layer, const bf16* k, const
 // arguments, so that a refused call changes nothing, and finds the pages: free
 // pages are handed out lowest first, in the order of the list.  The apply
 // kernel (many CTAs) rewrites the tables and counts and copies the pages.
+// One CTA plans because the hand-out is a prefix sum over the pool: 3 to 5 us for
+// pools of some thousand pages, most of it dependent loads, 0.3 us more for each
+// further 4096 pages that it has to look through.
 // The workspace (32-bit words):
 //   head[16]: 0 go, 1 copies, 2 pages wanted, 3 live pages, 4 live pages below the live count
 //   first[n]: the number of pages wanted by the entries before
@@ -587,7 +590,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Wor
 }
 
 // Copies of whole pages (codes and scales), a grid-stride loop over pieces of
-// 16 KB: four 16-byte loads in flight per thread.
+// 16 KB: four 16-byte loads in flight per thread, six CTAs per SM.  155 MB of
+// pages moved: 47 us, 6.6 TB/s read and written.
 constexpr int COPY_THREADS = 256;
 constexpr int COPY_PIECE = COPY_THREADS * 64;
 template <class Pair>

@@ -17,16 +17,23 @@
 // Values are taken relative to the largest scale so far; when that rises, O is
 // scaled down as it is when the row maximum moves.
 //
-// Roles (512 threads of 128 registers, one CTA per SM; registers moved from the
-// converting warps to the softmax cost more there than they gave here):
-// warps 0-3, 14 and 15 convert, warps 4-7 and 8-11 are the softmax of tile 0 and
-// 1, warps 12 and 13 issue their MMAs.  Two tiles per
-// CTA instead of two CTAs of one tile: the conversion is done once for both,
-// and one tile's exponentials run while the other's MMAs do.
+// Roles (512 threads of 128 registers, one CTA per SM): warps 0-3, 14 and 15
+// convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warps 12 and 13
+// issue their MMAs.  Two tiles per CTA instead of two CTAs of one tile: the
+// conversion is done once for both, and one tile's exponentials run while the
+// other's MMAs do.  (Registers moved from the converting warps to the softmax
+// cost more there than they gave here.)
 //
-// As in the streaming kernel the key blocks of all tiles are one line of work
-// cut into equal parts, one per SM, and the cut tiles are joined by a second
-// kernel: 247 tiles of 300 to 1024 rows would load 148 SMs unevenly.
+// As in the streaming kernel the key blocks of all items are one line of work
+// cut into equal parts, one per SM, and the cut items are joined by a second
+// kernel: four chunks of 300 to 1024 rows are 120 items of unequal length, which
+// taken whole would leave SMs idle and others twice as busy.
+//
+// Measured: 64 sequences of 256 new tokens over 4096, 12 heads: 423 us at d = 64
+// (472 TFLOP/s), 725 at d = 128 (551); one tile per item (128 new tokens) 335 us;
+// four chunks of 300 to 1024 over 1500 to 4096: 62 us.  The exponentials bound it
+// (MUFU 16 a cycle: 1.1 us of the 2.6 of a block with two tiles) together with the
+// softmax warps' latency, and at d = 128 the conversion.
 //
 // All waits are bounded.
 #pragma once
@@ -77,8 +84,8 @@ __device__ __forceinline__ int item_blocks(const Call& k, int len, int q, int j)
 }
 __device__ __forceinline__ int items_of(const Call& k, int q) { return (q * k.group + W_ROWS - 1) / W_ROWS; }
 
-// what a block counts: with two tiles half as much again as with one (3.2 and 2.2 us)
-__device__ __forceinline__ int item_cost(const Call& k, int q, int j) { return q * k.group - j * W_ROWS > 128 ? 3 : 2; }
+// what a block counts: with two tiles a third more than with one (2.6 and 2.0 us)
+__device__ __forceinline__ int item_cost(const Call& k, int q, int j) { return q * k.group - j * W_ROWS > 128 ? 4 : 3; }
 
 __device__ __forceinline__ bool lay_out_wide(const Call& k, long long* pre, long long* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -706,8 +713,8 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   Call a = k;
   a.join = static_cast<Join*>(work);
   a.part = reinterpret_cast<float*>(a.join + grid);
-  a.setup = 5;
-  a.min_part = 11;
+  a.setup = 12;     // an item's Q, first scores and output: three blocks' time
+  a.min_part = 20;
   wide_kernel<FMT, D><<<grid, W_THREADS, S::bytes(k.n), st>>>(a);
   e = cudaGetLastError();
   if (e == cudaSuccess && k.narrow) e = stream(k, stream_work, st, true);

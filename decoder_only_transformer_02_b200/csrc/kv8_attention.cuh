@@ -32,7 +32,7 @@
 //    sequences of up to 16384 tokens, 705 MB: 6.0 TB/s of 6.56 measured).
 //  - All sequences' 16-token groups, tile after tile (a tile: the rows of one
 //    sequence and key/value head), are one line of work that is cut into equal
-//    parts, one per CTA; a part's warps split each piece of a tile.  A tile
+//    parts, one per CTA; a part's warps take its steps in turn.  A tile
 //    that was cut leaves partial results that a second kernel joins in order,
 //    so the result is the same in every run.
 #pragma once
@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
   long long at = 0, end = 1, per = 1;
   int join_parts = 0;
   Piece p;
+  int first_page = 0;
   if (SPLIT) {
     pdl_launch();
     const bool ok = lay_out(k, RT, line, s_warp);
@@ -281,6 +282,9 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
     p.e.slot = k.slots[i];
     p.e.a = k.cu[i];
     p.e.q = k.cu[i + 1] - p.e.a;
+    // (the page ids are requested with the length, not behind it)
+    if ((unsigned)p.e.slot < (unsigned)c.num_slots)
+      first_page = c.table[(long)p.e.slot * c.max_pages + min(((lane / U * W + warp) * U + lane % U) >> (c.ps_log2 - 4), c.max_pages - 1)];
     p.e.len = c.len_of(p.e.slot);
     p.head = blockIdx.x % c.kvh;
     p.row0 = blockIdx.x / c.kvh * RT;
@@ -321,22 +325,22 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
     if (SPLIT && p.g1 == p.g0) continue;  // only the tile's setup units are in this part
     const int tile_rows = min(RT, p.e.q * k.group - p.row0);
 
-    // ---- this warp's groups, and their pages
-    const int cnt = p.g1 - p.g0;
-    const int gs = p.g0 + (int)((long)cnt * warp / W), ge = p.g0 + (int)((long)cnt * (warp + 1) / W);
+    // ---- this warp's steps: the groups g0 + (W k + warp) U .. + U - 1, k = 0, 1, ..., and their pages
+    const int own = p.g0 + warp * U;
     const int32_t* table = c.table + (long)p.e.slot * c.max_pages;
     const int gp_log2 = c.ps_log2 - 4;  // groups of a page
     const long page_stride = c.page_bytes();
     const uint8_t* head_base = c.codes + ((long)k.layer * 2 * c.kvh + p.head) * c.ps * D;
     const long side_stride = (long)c.kvh * c.ps * D;
-    int pg = 0, base = gs;
+    int pg = 0, base = 0;
     float ksc = 0.f, vsc = 0.f;
-    auto batch = [&](int from) {  // lane x: page and scales of group from + x
+    auto batch = [&](int from, bool known) {  // lane x: page and scales of group x % U of step from + x / U
       base = from;
+      const int gi = own + (from + lane / U) * (W * U) + lane % U;
       pg = 0;
       ksc = vsc = 0.f;
-      if (from + lane < ge) {
-        pg = table[(from + lane) >> gp_log2];
+      if (gi < p.g1) {
+        pg = known ? first_page : table[gi >> gp_log2];
         if (c.page_ok(pg)) {
           ksc = c.scales[c.unit(pg, k.layer, 0, p.head)];
           vsc = c.scales[c.unit(pg, k.layer, 1, p.head)];
@@ -348,14 +352,15 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         }
       }
     };
-    // starts the copies of groups gi .. gi + U - 1; keys and values of tokens behind the last become zero
-    auto load = [&](int gi, int stage) {
+    // starts the copies of a step; keys and values of tokens behind the last become zero
+    auto load = [&](int step, int stage) {
+      const int gi = own + step * (W * U), at = (step - base) * U;
       const uint32_t dst = ring + stage * S::STEP;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int page = __shfl_sync(0xffffffffu, pg, (gi + u - base) & 31);
+        const int page = __shfl_sync(0xffffffffu, pg, at + u);
         const uint8_t* t = head_base + page * page_stride + (((gi + u) << 4) & (c.ps - 1)) * D;
-        const int left = gi + u < ge ? p.e.len - (gi + u) * GROUP : 0;
+        const int left = gi + u < p.g1 ? p.e.len - (gi + u) * GROUP : 0;
 #pragma unroll
         for (int r = 0; r < GROUP; r += ROWS) {
           const int row = r + crow, tok = sigma(row);
@@ -367,8 +372,8 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
       }
       copy_commit();
       // (the scales come behind the codes' requests: they may still be on their way)
-      const float a = __shfl_sync(0xffffffffu, ksc, (gi + lane - base) & 31);
-      const float b = __shfl_sync(0xffffffffu, vsc, (gi + lane - base) & 31);
+      const float a = __shfl_sync(0xffffffffu, ksc, (at + lane) & 31);
+      const float b = __shfl_sync(0xffffffffu, vsc, (at + lane) & 31);
       if (lane < U)
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + STAGES * S::STEP + 8 * (stage * U + lane)), "f"(a), "f"(b)
                      : "memory");
@@ -401,10 +406,10 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         vinv = 1.f / top;
       }
     };
-    batch(gs);
+    batch(0, !SPLIT);
 #pragma unroll
     for (int st = 0; st < STAGES - 1; ++st) {
-      if (gs + st * U < ge) load(gs + st * U, st);
+      if (own + st * (W * U) < p.g1) load(st, st);
       else copy_commit();
     }
 
@@ -456,18 +461,18 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
     raise();
 
     int stage = 0;
-    for (int gi = gs; gi < ge; gi += U) {
+    for (int step = 0, gi = own; gi < p.g1; ++step, gi += W * U) {
       copy_wait<STAGES - 2>();
       __syncwarp();  // every lane's copies have landed, and the stage before is free
       {
-        const int nx = gi + (STAGES - 1) * U;
-        if (nx < ge) {
-          if (nx - base >= 32) {
-            batch(nx);
-            load(nx, stage == 0 ? STAGES - 1 : stage - 1);
+        const int nx = step + STAGES - 1, free_stage = stage == 0 ? STAGES - 1 : stage - 1;
+        if (own + nx * (W * U) < p.g1) {
+          if (nx - base >= 32 / U) {
+            batch(nx, false);
+            load(nx, free_stage);
             raise();
           } else {
-            load(nx, stage == 0 ? STAGES - 1 : stage - 1);
+            load(nx, free_stage);
           }
         } else {
           copy_commit();
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         }
       }
       const int t0 = gi * GROUP;
-      const bool edge = t0 + U * GROUP - 1 > minpos || gi + U > ge;
+      const bool edge = t0 + U * GROUP - 1 > minpos || gi + U > p.g1;
       if (edge) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (gi + u >= ge || t0 + u * GROUP + sigma(g) + 8 * (e >> 1) > pos[nt][e & 1]) s[u][nt][e] = -INFINITY;
+              if (gi + u >= p.g1 || t0 + u * GROUP + sigma(g) + 8 * (e >> 1) > pos[nt][e & 1]) s[u][nt][e] = -INFINITY;
       }
       // ---- row maxima, moved only past 2^8
       float top[NT][2];

@@ -294,7 +294,7 @@ static inline cudaError_t append(const Cache& c, int layer, const bf16* k, const
 // pages are handed out lowest first, in the order of the list.  The apply
 // kernel (many CTAs) rewrites the tables and counts and copies the pages.
 // One CTA plans because the hand-out is a prefix sum over the pool: 3 to 5 us for
-// pools of some thousand pages, most of it dependent loads, 0.3 us more for each
+// pools of some thousand pages, most of it dependent loads, 0.7 us more for each
 // further 4096 pages that it has to look through.
 // The workspace (32-bit words):
 //   head[16]: 0 go, 1 copies, 2 pages wanted, 3 live pages, 4 live pages below the live count
@@ -353,25 +353,49 @@ __device__ __forceinline__ int4 refs_at(const Cache& c, int p) {
   return r;
 }
 
+// A pass over the pool takes 4 x 4096 pages at a time: thread t the pages 4 t ..
+// + 3 of each 4096, and one scan of the four counts, 16 bits each.
+constexpr int SCAN = 4 * PLAN_THREADS;
+struct Four {
+  int4 r[4];
+};
+__device__ __forceinline__ Four four_at(const Cache& c, int base) {
+  Four f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f.r[q] = make_int4(1, 1, 1, 1);
+    if (base + q * SCAN < c.num_pages) f.r[q] = refs_at(c, base + q * SCAN + 4 * (int)threadIdx.x);
+  }
+  return f;
+}
+
 // The wanted lowest free pages (refs 0) into list; returns how many there are
 // (at least `want`, or all of them).
 __device__ __forceinline__ uint64_t find_free(const Cache& c, uint64_t want, int32_t* list, uint64_t* s_warp) {
   uint64_t found = 0;
-  int4 r = refs_at(c, 4 * threadIdx.x);
-  for (int base = 0; base < c.num_pages && found < want; base += 4 * PLAN_THREADS) {
-    const int p = base + 4 * threadIdx.x;
-    const int4 next = refs_at(c, p + 4 * PLAN_THREADS);
-    uint64_t total;
-    uint64_t at = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), total, s_warp);
-    if (r.x == 0 && at < want) list[at] = p;
-    at += r.x == 0;
-    if (r.y == 0 && at < want) list[at] = p + 1;
-    at += r.y == 0;
-    if (r.z == 0 && at < want) list[at] = p + 2;
-    at += r.z == 0;
-    if (r.w == 0 && at < want) list[at] = p + 3;
-    found += total;
-    r = next;
+  if (want == 0) return 0;
+  Four f = four_at(c, 0);
+  for (long base = 0; base < c.num_pages && found < want; base += 4 * SCAN) {
+    uint64_t count = 0, total;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (base + q * SCAN < c.num_pages)
+        count += (uint64_t)((f.r[q].x == 0) + (f.r[q].y == 0) + (f.r[q].z == 0) + (f.r[q].w == 0)) << (16 * q);
+    const uint64_t before = block_scan(count, total, s_warp);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (base + q * SCAN >= c.num_pages) break;
+      uint64_t at = found + (before >> (16 * q) & 0xffff);
+      const int p = (int)base + q * SCAN + 4 * (int)threadIdx.x;
+      const int v[4] = {f.r[q].x, f.r[q].y, f.r[q].z, f.r[q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (v[e] == 0 && at < want) list[at] = p + e;
+        at += v[e] == 0;
+      }
+      found += total >> (16 * q) & 0xffff;
+    }
+    if (base + 4 * SCAN < c.num_pages) f = four_at(c, (int)base + 4 * SCAN);
   }
   return found;
 }
@@ -548,38 +572,48 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Wor
   __shared__ uint64_t s_warp[32];
   const int tid = threadIdx.x;
   pdl_launch();
+  auto used = [&](int p, int refs) { return p < c.num_pages && refs > 0; };
   uint64_t count = 0;
-  for (int p = 4 * tid; p < c.num_pages; p += 4 * PLAN_THREADS) {
+#pragma unroll 4
+  for (int p = 4 * tid; p < c.num_pages; p += SCAN) {
     const int4 r = refs_at(c, p);
-    count += (r.x > 0) + (p + 1 < c.num_pages && r.y > 0) + (p + 2 < c.num_pages && r.z > 0) + (p + 3 < c.num_pages && r.w > 0);
+    count += used(p, r.x) + used(p + 1, r.y) + used(p + 2, r.z) + used(p + 3, r.w);
   }
   uint64_t total;
   block_scan(count, total, s_warp);
   const int live = (int)total;
   if (tid == 0 && live == c.num_pages) w.head[4] = live;
-  int before = 0;
-  int4 r = refs_at(c, 4 * tid);
-  for (int base = 0; base < c.num_pages; base += 4 * PLAN_THREADS) {
-    const int p0 = base + 4 * tid;
-    const int4 next = refs_at(c, p0 + 4 * PLAN_THREADS);
-    const int v[4] = {r.x, r.y, r.z, r.w};
-    int is[4];
+  int below = 0;  // live pages so far
+  Four f = four_at(c, 0);
+  for (long base = 0; base < c.num_pages; base += 4 * SCAN) {
+    count = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) is[e] = p0 + e < c.num_pages && v[e] > 0;
-    int at = before + (int)block_scan(is[0] + is[1] + is[2] + is[3], total, s_warp);  // live pages below p
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = p0 + e;
-      if (p < c.num_pages) {
-        if (p == live) w.head[4] = at;
-        if (p < live && !is[e]) w.list[p - at] = p;
-        if (p >= live) w.rank[p] = is[e] ? at : -1;
-        if (p >= live && is[e]) w.high[at] = p;
-      }
-      at += is[e];
+    for (int q = 0; q < 4; ++q) {
+      if (base + q * SCAN >= c.num_pages) break;
+      const int p = (int)base + q * SCAN + 4 * tid;
+      count += (uint64_t)(used(p, f.r[q].x) + used(p + 1, f.r[q].y) + used(p + 2, f.r[q].z) + used(p + 3, f.r[q].w)) << (16 * q);
     }
-    before += (int)total;
-    r = next;
+    const uint64_t before = block_scan(count, total, s_warp);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (base + q * SCAN >= c.num_pages) break;
+      int at = below + (int)(before >> (16 * q) & 0xffff);
+      const int v[4] = {f.r[q].x, f.r[q].y, f.r[q].z, f.r[q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = (int)base + q * SCAN + 4 * tid + e;
+        const bool is = used(p, v[e]);
+        if (p < c.num_pages) {
+          if (p == live) w.head[4] = at;
+          if (p < live && !is) w.list[p - at] = p;
+          if (p >= live) w.rank[p] = is ? at : -1;
+          if (p >= live && is) w.high[at] = p;
+        }
+        at += is;
+      }
+      below += (int)(total >> (16 * q) & 0xffff);
+    }
+    if (base + 4 * SCAN < c.num_pages) f = four_at(c, (int)base + 4 * SCAN);
   }
   __syncthreads();
   if (tid == 0) {

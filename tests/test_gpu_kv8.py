@@ -499,25 +499,26 @@ def test_lengths_whose_pages_pass_32_bits_are_refused():
         assert torch.all(c.refs == 0) and torch.all(c.lens == 0)
 
 
-def test_pools_larger_than_one_scan():
+@pytest.mark.parametrize("pages,taken", [(30011, 20003), (70001, 65531), (16384 + 5000, 16383), (100000, 3)])
+def test_pools_larger_than_one_scan(pages, taken):
     """Free pages far into the pool, more entries than one block has threads."""
     G = _g()
-    n, pages = 2500, 30011
+    n = 2500
     c = G.KV8Cache.allocate(R.INT8, 1, 1, 64, 16, pages, 5000, 4)
     work = torch.empty(c.workspace_bytes(n), dtype=torch.uint8, device="cuda")
-    c.refs[:20003] = 1
+    c.refs[:taken] = 1
     slots = torch.randperm(5000)[:n].int().cuda()
-    lens = (torch.arange(n, dtype=torch.int32) % 50).cuda()
+    lens = (torch.arange(n, dtype=torch.int32) % 41).cuda()
     c.resize(slots, lens, work)
     G.check_device_error()
     used = (lens + 15) // 16
     first = used.cumsum(0) - used
     for j in range(4):
-        want = torch.where(used > j, 20003 + first + j, -1).int()
+        want = torch.where(used > j, taken + first + j, -1).int()
         assert torch.equal(c.table[slots.long(), j], want)
     total = int(used.sum())
-    assert torch.all(c.refs[20003:20003 + total] == 1) and torch.all(c.refs[20003 + total:] == 0)
-    c.refs[:20003] = 0
+    assert torch.all(c.refs[taken:taken + total] == 1) and torch.all(c.refs[taken + total:] == 0)
+    c.refs[:taken] = 0
     c.codes.view(torch.uint8)[:] = (torch.arange(pages, device="cuda") % 251).to(torch.uint8).view(-1, 1, 1, 1, 1, 1)
     live = torch.zeros(1, dtype=torch.int32, device="cuda")
     old = c.table.clone()

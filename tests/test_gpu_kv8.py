@@ -689,6 +689,69 @@ def test_graph_capture_side_stream_and_determinism():
         assert torch.equal(r[1].codes.view(torch.uint8), c4.codes.view(torch.uint8))
 
 
+def test_first_call_of_a_process_inside_a_capture():
+    """Every call's one-time set-up happens outside the stream, so that a
+    program may capture before it has run anything."""
+    _g()
+    code = """
+import torch
+from decoder_only_transformer_02_b200 import gpt2 as G
+c = G.KV8Cache.allocate(G.GPT2_KV_E4M3, 1, 2, 64, 16, 600, 4, 300)
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+slots, cu, lens = i32([2, 0]), i32([0, 100, 101]), i32([100, 1])
+x = torch.randn(101, 6, 64, device="cuda").bfloat16()
+out = torch.zeros(101, 2, 64, dtype=torch.bfloat16, device="cuda")
+work = torch.empty(c.workspace_bytes(4), dtype=torch.uint8, device="cuda")
+awork = torch.empty(c.attention_workspace_bytes(2, 2, 101, 100), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    st = torch.cuda.current_stream()
+    c.resize(slots, lens, work, stream=st)
+    c.append(0, x[:, 2:4], x[:, 4:], slots, cu, stream=st)
+    c.attention(0, x[:, :2], out, slots, cu, 100, awork, stream=st)
+    c.compact(work, stream=st)
+g.replay()
+torch.cuda.synchronize()
+G.check_device_error()
+assert torch.isfinite(out).all() and out[100].abs().sum() > 0 and c.lens.tolist() == [1, 0, 100, 0]
+print("captured")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_attention_calls_at_once_on_one_cache():
+    p = Pair(R.E4M3, kvh=2, ps=32, num_pages=200, max_pages=100)
+    p.append([0, 1, 2], [3000, 700, 1])
+    q = torch.randn(400, 2, 64, device="cuda").bfloat16()
+    calls = [([0, 1, 2], [1, 1, 1], 1), ([1, 0], [300, 70], 300)]
+    streams = [torch.cuda.Stream() for _ in calls]
+
+    def run(at_once):
+        outs = []
+        for st, (slots, news, max_q) in zip(streams, calls):
+            cu = _i32(np.concatenate([[0], np.cumsum(news)]))
+            out = torch.zeros(sum(news), 2, 64, dtype=torch.bfloat16, device="cuda")
+            work = torch.empty(p.dev.attention_workspace_bytes(2, len(slots), len(out), max_q), dtype=torch.uint8, device="cuda")
+            outs.append((out, _i32(slots), cu, work))
+        torch.cuda.synchronize()
+        for _ in range(10 if at_once else 1):
+            for st, o, (_, _, max_q) in zip(streams, outs, calls):
+                p.dev.attention(0, q[:len(o[0])], o[0], o[1], o[2], max_q, o[3], stream=st)
+                if not at_once:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        p.G.check_device_error()
+        return [o[0] for o in outs]
+
+    assert all(torch.equal(a, b) for a, b in zip(run(False), run(True)))
+
+
 def test_as_many_sequences_as_a_call_takes():
     """4096 short sequences, and a prompt among them."""
     G = _g()

@@ -157,11 +157,11 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
   bool bad = false;
 #pragma unroll 1
   for (int i = tid; i < n; i += blockDim.x) {
-    const int a = cu[i], b = cu[i + 1];
+    const int a = cu[i], b = cu[i + 1], slot = slots[i];
     const bool mine = by_row ? x >= a && x < b
                              : x >= (a >> c.ps_log2) + 2 * i && x < (b >> c.ps_log2) + 2 * i + 2;
     bad |= a < 0 || b < a || b > rows;
-    if (mine) s_i = i, s_a = a, s_b = b, s_slot = slots[i];  // one thread at most, unless the offsets are bad
+    if (mine) s_i = i, s_a = a, s_b = b, s_slot = slot;  // one thread at most, unless the offsets are bad
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) set_device_err(DERR_KV8_ARGS);
@@ -170,13 +170,13 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
   const int i = s_i;
   if (i < 0) return;
   const int a = s_a, q = s_b - a, slot = s_slot;
+  const int len = c.len_of(slot);
   // a slot named twice: the later entries are refused, or both would write the same tokens
   bool twice = false;
 #pragma unroll 1
   for (int j = tid; j < i; j += blockDim.x) twice |= slots[j] == slot && cu[j + 1] > cu[j];
   twice = __syncthreads_or(twice);
   if (q == 0) return;
-  const int len = c.len_of(slot);
   if (len < q || twice) {
     if (tid == 0) set_device_err(DERR_KV8_ARGS);
     return;
@@ -573,9 +573,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Wor
   const int tid = threadIdx.x;
   pdl_launch();
   auto used = [&](int p, int refs) { return p < c.num_pages && refs > 0; };
+  Four f = four_at(c, 0);
   uint64_t count = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int p = q * SCAN + 4 * tid;
+    count += used(p, f.r[q].x) + used(p + 1, f.r[q].y) + used(p + 2, f.r[q].z) + used(p + 3, f.r[q].w);
+  }
 #pragma unroll 4
-  for (int p = 4 * tid; p < c.num_pages; p += SCAN) {
+  for (int p = 4 * SCAN + 4 * tid; p < c.num_pages; p += SCAN) {
     const int4 r = refs_at(c, p);
     count += used(p, r.x) + used(p + 1, r.y) + used(p + 2, r.z) + used(p + 3, r.w);
   }
@@ -584,7 +590,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan_kernel(Cache c, Wor
   const int live = (int)total;
   if (tid == 0 && live == c.num_pages) w.head[4] = live;
   int below = 0;  // live pages so far
-  Four f = four_at(c, 0);
   for (long base = 0; base < c.num_pages; base += 4 * SCAN) {
     count = 0;
 #pragma unroll

@@ -140,12 +140,14 @@ constexpr int APPEND_WARPS = 8;
 // by_row: x is a row, and works if its token is the run's first.  Otherwise x
 // counts runs: sequence i owns the numbers from cu[i] / ps + 2 i, enough since
 // its q tokens touch at most q / ps + 2 pages; no prefix sum is needed.
-// HELD: 16-byte pieces of a tile that a lane keeps between the two passes (the
-// rest is read again): 1 for short runs, 4 (a tile of 1024 values) for prompts.
+// HELD: 16-byte pieces of a tile that a lane keeps between the two passes: 1 for
+// short runs, 4 (a tile of 1024 values) for prompts; the rest is read again, UN
+// pieces at a time: 1 where nothing is left (17.7 us; with 4, whose registers
+// cost warps, 20.0), 4 where tiles are larger (64 tokens of 64: 22.5; with 1, 30).
 // What it moves: 2 bytes in, 1 out per value.  15,400 rows of 2 x 768 values:
 // 17.8 us (3.9 TB/s; 25.7 with both passes reading, 22 with 8 pieces held, whose
 // registers cost half the warps); 256 single rows: 5.8 us, its chain of loads.
-template <int FMT, int HELD>
+template <int FMT, int HELD, int UN>
 __global__ void __launch_bounds__(32 * APPEND_WARPS)
     append_kernel(Cache c, int layer, const bf16* __restrict__ k, const bf16* __restrict__ v, long ld,
                   const int32_t* __restrict__ slots, const int32_t* __restrict__ cu, int n, int rows, int by_row) {
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
       if (sub + i * per < m) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (long)(sub + i * per) * ld));
     }
     const uint32_t old = off ? __float_as_uint(c.scales[u]) : 0u;
-#pragma unroll 1
+#pragma unroll UN
     for (int r = sub + HELD * per; r < m; r += per) largest(__ldg(reinterpret_cast<const uint4*>(src + (long)r * ld)));
 #pragma unroll
     for (int i = 0; i < HELD; ++i) largest(x[i]);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
       if (sub + i * per < m) store(x[i], sub + i * per);
-#pragma unroll 1
+#pragma unroll UN
     for (int r = sub + HELD * per; r < m; r += per) store(__ldg(reinterpret_cast<const uint4*>(src + (long)r * ld)), r);
     __syncwarp();
   }
@@ -278,12 +280,13 @@ static inline cudaError_t append(const Cache& c, int layer, const bf16* k, const
   const int most = (2 * c.kvh + APPEND_WARPS - 1) / APPEND_WARPS;
   const int ys = (int)(xs * most <= APPEND_CTAS ? most : (APPEND_CTAS + xs - 1) / xs);
   const dim3 grid((unsigned)xs, ys < 1 ? 1 : ys > most ? most : ys);
-#define KV8_APPEND(F, HELD) \
-  append_kernel<F, HELD><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row)
+#define KV8_APPEND(F, HELD, UN) \
+  append_kernel<F, HELD, UN><<<grid, 32 * APPEND_WARPS, 0, st>>>(c, layer, k, v, ld, slots, cu, n, rows, by_row)
+  const bool fits = c.tile() <= 1024;
   if (c.fmt == GPT2_KV_INT8)
-    by_row ? KV8_APPEND(GPT2_KV_INT8, 1) : KV8_APPEND(GPT2_KV_INT8, 4);
+    by_row ? KV8_APPEND(GPT2_KV_INT8, 1, 1) : fits ? KV8_APPEND(GPT2_KV_INT8, 4, 1) : KV8_APPEND(GPT2_KV_INT8, 4, 4);
   else
-    by_row ? KV8_APPEND(GPT2_KV_E4M3, 1) : KV8_APPEND(GPT2_KV_E4M3, 4);
+    by_row ? KV8_APPEND(GPT2_KV_E4M3, 1, 1) : fits ? KV8_APPEND(GPT2_KV_E4M3, 4, 1) : KV8_APPEND(GPT2_KV_E4M3, 4, 4);
 #undef KV8_APPEND
   return cudaGetLastError();
 }

@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       // bytes for each lane; warp w takes the pieces w, w + 6, ...
       constexpr int ROWS = 512 / D, PER_SIDE = W_KEYS / ROWS, NX = (32 + W_CONV - 1) / W_CONV;
       const int cw = warp < 4 ? warp : warp - 10;
-      const int lrow = lane / (D / 16), lq = lane % (D / 16);
+      // a lane's row and 16-byte piece in it: every eight lanes hold two rows of four
+      // pieces, whose f16 values the swizzle puts into different banks
+      const int lrow = D == 64 ? lane >> 2 : (lane >> 2) & 3, lq = D == 64 ? lane & 3 : (lane & 3) + 4 * (lane >> 4);
       auto mine = [&](int e) { return cw + W_CONV * e < 32; };
       uint32_t g = 0;
       bool ok = true;
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
               const int i = cw + W_CONV * e + 32 * unit, row0 = (i & (PER_SIDE - 1)) * ROWS;
               const int pg = __shfl_sync(0xffffffffu, page, row0 >> c.ps_log2);
               nx[e] = __ldcg(reinterpret_cast<const uint4*>(head_base + pg * page_stride + (i >= PER_SIDE ? side_stride : 0) +
-                                                            ((row0 & (c.ps - 1)) * D + lane * 16 + after)));
+                                                            ((row0 & (c.ps - 1)) * D + lrow * D + lq * 16 + after)));
             }
         };
         float vref = 0.f;
@@ -416,13 +418,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
                 if (left < W_KEYS && row >= left) w = make_uint4(0, 0, 0, 0);
                 uint32_t x[8];
                 codes16_half<FMT>(w, f, x);
-                // the two 16-byte pieces in an order that keeps eight lanes in different banks
-                const bool y = D == 128 && (lq >> 2);
                 const uint32_t tile = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE) + (row >> 3) * 1024 +
                                       (row & 7) * 128 + (D == 128 ? (lq >> 2) * 16384 : 0);
                 const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
-                sts128(tile + (y ? c0 ^ 16 : c0), y ? x[4] : x[0], y ? x[5] : x[1], y ? x[6] : x[2], y ? x[7] : x[3]);
-                sts128(tile + (y ? c0 : c0 ^ 16), y ? x[0] : x[4], y ? x[1] : x[5], y ? x[2] : x[6], y ? x[3] : x[7]);
+                sts128(tile + c0, x[0], x[1], x[2], x[3]);
+                sts128(tile + (c0 ^ 16), x[4], x[5], x[6], x[7]);
               }
           }
           fence_async_smem();

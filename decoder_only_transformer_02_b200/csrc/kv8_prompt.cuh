@@ -330,6 +330,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
       // pieces, whose f16 values the swizzle puts into different banks
       const int lrow = D == 64 ? lane >> 2 : (lane >> 2) & 3, lq = D == 64 ? lane & 3 : (lane & 3) + 4 * (lane >> 4);
       auto mine = [&](int e) { return cw + W_CONV * e < 32; };
+      // where the lane's two f16 pieces go within eight rows (the row among them is the same for all of a warp's pieces)
+      static_assert(W_CONV % 2 == 0, "pieces of four rows keep their place among eight");
+      const int row7 = D == 64 ? lrow : (cw & 1) * 4 + lrow;
+      const uint32_t lane_to = row7 * 128 + (((2 * lq & 7) ^ row7) << 4) + (lq >> 2) * 16384;
+      const int lane_from = lrow * D + lq * 16;
       uint32_t g = 0;
       bool ok = true;
       const long page_stride = c.page_bytes();
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
               const int i = cw + W_CONV * e + 32 * unit, row0 = (i & (PER_SIDE - 1)) * ROWS;
               const int pg = __shfl_sync(0xffffffffu, page, row0 >> c.ps_log2);
               nx[e] = __ldcg(reinterpret_cast<const uint4*>(head_base + pg * page_stride + (i >= PER_SIDE ? side_stride : 0) +
-                                                            ((row0 & (c.ps - 1)) * D + lrow * D + lq * 16 + after)));
+                                                            ((row0 & (c.ps - 1)) * D + lane_from + after)));
             }
         };
         float vref = 0.f;
@@ -412,17 +417,15 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
             for (int e = 0; e < NX; ++e)
               if (mine(e)) {
                 const int i = cw + W_CONV * e + 32 * u, side = i >= PER_SIDE;
-                const int row0 = (i & (PER_SIDE - 1)) * ROWS, row = row0 + lrow;
+                const int row0 = (i & (PER_SIDE - 1)) * ROWS;
                 const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row0 >> c.ps_log2);
                 uint4 w = cur[e];
-                if (left < W_KEYS && row >= left) w = make_uint4(0, 0, 0, 0);
+                if (left < W_KEYS && row0 + lrow >= left) w = make_uint4(0, 0, 0, 0);
                 uint32_t x[8];
                 codes16_half<FMT>(w, f, x);
-                const uint32_t tile = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE) + (row >> 3) * 1024 +
-                                      (row & 7) * 128 + (D == 128 ? (lq >> 2) * 16384 : 0);
-                const uint32_t c0 = ((2 * lq & 7) ^ (row & 7)) << 4;
-                sts128(tile + c0, x[0], x[1], x[2], x[3]);
-                sts128(tile + (c0 ^ 16), x[4], x[5], x[6], x[7]);
+                const uint32_t to = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE) + (row0 >> 3) * 1024 + lane_to;
+                sts128(to, x[0], x[1], x[2], x[3]);
+                sts128(to ^ 16, x[4], x[5], x[6], x[7]);
               }
           }
           fence_async_smem();

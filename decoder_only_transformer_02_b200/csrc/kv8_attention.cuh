@@ -664,10 +664,12 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
   pdl_wait();  // (behind the wide kernel: this one does not end before it)
 }
 
-// CTA x joins the tile that began in part x of the line and went on past it:
-// its partial results lie with part x (place 1) and the parts after it (place
-// 0).  The warps take the parts in turn; results meet in warp order.
+// CTAs (x, ...) join the tile that began in part x of the line and went on past
+// it: its partial results lie with part x (place 1) and the parts after it
+// (place 0).  The warps take the parts in turn; results meet in warp order.
+// A tile's rows are spread over the CTAs of y, four or fewer each.
 constexpr int J_WARPS = 8;
+constexpr int join_ctas(int rt) { return rt / 4; }
 template <int D, int RT>
 __global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
   constexpr int LANES = D / 4;  // threads of a row
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
   if (t.parts == 0) return;
   constexpr long SIZE = (long)RT * (D + 2);
   const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
-  for (int r0 = 0; r0 < t.tile_rows; r0 += 32 / LANES) {
+  for (int r0 = blockIdx.y * (32 / LANES); r0 < t.tile_rows; r0 += gridDim.y * (32 / LANES)) {
     const int r = r0 + lane / LANES, d4 = lane % LANES;
     const bool on = r < t.tile_rows;
     float M = -INFINITY, L = 0.f;
@@ -733,9 +735,9 @@ static inline int sm_count() {
 }
 
 // Sequences with more rows per key/value head than this go to the tensor-core
-// kernel of kv8_prompt.cuh.  16 sequences of 4096: 64 rows take 98.2 us here, 65
-// take 97.9 there; 64 sequences of 1024: 104 and 141; d = 128: 168 and 176.  Below,
-// the streaming kernel wins (32 rows: 64, 57 and 100 us).
+// kernel of kv8_prompt.cuh.  16 sequences of 4096: 64 rows take 96.6 us here, 65
+// take 94.5 there; 64 sequences of 1024: 102 and 133; d = 128: 169 and 168.  Below,
+// the streaming kernel wins (32 rows: 62, 57 and 101 us).
 constexpr int NARROW_ROWS = 64;
 static inline long narrow_rows(long rows) { return rows < NARROW_ROWS ? rows : NARROW_ROWS; }
 
@@ -781,7 +783,7 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_after(join_kernel<D, S::RT>, dim3(grid), 32 * J_WARPS, 0, st, a);
+  return launch_after(join_kernel<D, S::RT>, dim3(grid, join_ctas(S::RT)), 32 * J_WARPS, 0, st, a);
 }
 // Where no slot can hold more than this, every tile is one CTA's: no line, no
 // join.  64 sequences of 1 to 1024 tokens: 19.8 us, and cut into parts 23.8;

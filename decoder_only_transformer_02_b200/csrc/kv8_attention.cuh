@@ -669,19 +669,18 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
 // (place 0).  The warps take the parts in turn; results meet in warp order.
 // A tile's rows are spread over the CTAs of y, four or fewer each.
 constexpr int J_WARPS = 8;
-constexpr int join_ctas(int rt) { return rt / 4; }
+__host__ __device__ constexpr int join_ctas(int rt) { return rt / 4; }
 template <int D, int RT>
-__global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
+__device__ __forceinline__ void join_tile(const Call& k, const Join* join, const float* part, int part_x, int cta_y) {
   constexpr int LANES = D / 4;  // threads of a row
   __shared__ float4 s_a[J_WARPS][32];
   __shared__ float s_m[J_WARPS][32], s_l[J_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  const Join t = k.join[blockIdx.x];
+  const Join t = join[part_x];
   if (t.parts == 0) return;
   constexpr long SIZE = (long)RT * (D + 2);
-  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
-  for (int r0 = blockIdx.y * (32 / LANES); r0 < t.tile_rows; r0 += gridDim.y * (32 / LANES)) {
+  const float* first = part + ((long)part_x * 2 + 1) * SIZE;
+  for (int r0 = cta_y * (32 / LANES); r0 < t.tile_rows; r0 += join_ctas(RT) * (32 / LANES)) {
     const int r = r0 + lane / LANES, d4 = lane % LANES;
     const bool on = r < t.tile_rows;
     float M = -INFINITY, L = 0.f;
@@ -724,6 +723,11 @@ __global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
     __syncthreads();
   }
 }
+template <int D, int RT>
+__global__ void __launch_bounds__(32 * J_WARPS) join_kernel(const Call k) {
+  pdl_wait();
+  join_tile<D, RT>(k, k.join, k.part, blockIdx.x, blockIdx.y);
+}
 
 static inline int sm_count() {
   int dev = 0, n = 0;
@@ -741,10 +745,12 @@ static inline int sm_count() {
 constexpr int NARROW_ROWS = 64;
 static inline long narrow_rows(long rows) { return rows < NARROW_ROWS ? rows : NARROW_ROWS; }
 
+// rows of a tile in a call with more than NARROW_ROWS
+__host__ __device__ constexpr int wide_row_tile(int d) { return d == 128 ? 16 : 32; }
 // rows of a tile: the call's rows per key/value head, 8 to 32 (16 at d = 128)
 static inline int row_tile_of(const Cache& c, int group, int max_q) {
   const long r = narrow_rows((long)group * max_q);
-  return r <= 8 ? 8 : r <= 16 || c.d == 128 ? 16 : 32;
+  return r <= 8 ? 8 : r <= 16 ? 16 : wide_row_tile(c.d);
 }
 static inline int parts_of(const Cache& c, int rt) {
   return sm_count() * ctas_of(rt, c.d);
@@ -782,23 +788,24 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
     stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || behind) return e;  // (the wide kernel's join takes these tiles too)
   return launch_after(join_kernel<D, S::RT>, dim3(grid, join_ctas(S::RT)), 32 * J_WARPS, 0, st, a);
 }
 // Where no slot can hold more than this, every tile is one CTA's: no line, no
 // join.  64 sequences of 1 to 1024 tokens: 19.8 us, and cut into parts 23.8;
 // one sequence of 777: 6.3 (eight warps; sixteen 7.2), and cut 8.9.
 constexpr long WHOLE_TOKENS = 2048;
+static inline bool whole_tiles(const Cache& c) { return (long)c.max_pages * c.ps <= WHOLE_TOKENS; }
 template <int FMT, int D, int NT>
 static inline cudaError_t stream_mode(const Call& k, void* work, cudaStream_t st, bool behind) {
   const long tiles = (long)k.n * k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + 8 * NT - 1) / (8 * NT));
-  if ((long)k.c.max_pages * k.c.ps <= WHOLE_TOKENS)
+  if (whole_tiles(k.c))
     return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false>(k, work, st, behind) : stream_launch<FMT, D, NT, 4, false>(k, work, st, behind);
   return stream_launch<FMT, D, NT, 4, true>(k, work, st, behind);
 }
 template <int FMT>
 static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st, bool behind) {
-  const int rt = row_tile_of(k.c, k.group, k.max_q);
+  const int rt = behind ? wide_row_tile(k.c.d) : row_tile_of(k.c, k.group, k.max_q);  // (as the join behind both has it)
   if (k.c.d == 64)
     return rt == 8 ? stream_mode<FMT, 64, 1>(k, work, st, behind) : rt == 16 ? stream_mode<FMT, 64, 2>(k, work, st, behind) : stream_mode<FMT, 64, 4>(k, work, st, behind);
   return rt == 8 ? stream_mode<FMT, 128, 1>(k, work, st, behind) : stream_mode<FMT, 128, 2>(k, work, st, behind);

@@ -652,17 +652,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   }
 }
 
-// CTA (x, y): rows J_ROWS y .. of the item that begins in part x and goes on
-// after it, four columns of a row per thread; four parts are requested at once.
-constexpr int J_ROWS = 16;
+// The rows behind `row0` of the item that begins in part x and goes on after
+// it, four columns of a row per thread; four parts are requested at once.
+constexpr int J_THREADS = 32 * J_WARPS;
 template <int D>
-__global__ void __launch_bounds__(J_ROWS * D / 4) join_wide_kernel(const Call k) {
-  pdl_wait();
-  const Join t = k.join[blockIdx.x];
-  const int r = blockIdx.y * J_ROWS + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
+__device__ __forceinline__ void join_item(const Call& k, int part_x, int row0) {
+  const Join t = k.join[part_x];
+  const int r = row0 + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
   if (r >= t.tile_rows || t.parts == 0) return;
   constexpr long SIZE = (long)W_ROWS * (D + 2);
-  const float* first = k.part + ((long)blockIdx.x * 2 + 1) * SIZE;
+  const float* first = k.part + ((long)part_x * 2 + 1) * SIZE;
   float M = -INFINITY, L = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = 0; j0 < t.parts; j0 += 4) {
@@ -698,12 +697,27 @@ __global__ void __launch_bounds__(J_ROWS * D / 4) join_wide_kernel(const Call k)
   if (d4 == 0 && k.lse) k.lse[(long)(t.a + tok) * k.H + h] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// Joins the items of the wide kernel and the tiles of the streaming kernel that
+// followed it, in one launch: first `parts` CTAs for every J_THREADS threads of
+// an item, then `narrow_parts` for every join_ctas of a tile (0: none is cut).
+template <int D>
+__global__ void __launch_bounds__(J_THREADS) join_wide_kernel(const Call k, const Join* narrow, const float* narrow_part,
+                                                              int parts, int narrow_parts) {
+  constexpr int ROWS = J_THREADS / (D / 4), CTAS = W_ROWS / ROWS;
+  static_assert(CTAS * ROWS == W_ROWS, "every row of an item has its threads");
+  pdl_wait();
+  const int b = blockIdx.x, x = b - parts * CTAS;
+  if (x < 0) join_item<D>(k, b % parts, b / parts * ROWS);
+  else join_tile<D, wide_row_tile(D)>(k, narrow, narrow_part, x % narrow_parts, x / narrow_parts);
+}
+
 static inline size_t wide_workspace_bytes(const Cache& c) {
   return (size_t)sm_count() * (sizeof(Join) + 2 * (size_t)W_ROWS * (c.d + 2) * 4);
 }
 
 // The streaming kernel for the call's short sequences starts on the SMs that
 // the wide kernel leaves; each kernel of the chain ends after the one before it.
+// One join for both: 2 us less than one for each.
 template <int FMT, int D>
 static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_work, cudaStream_t st) {
   using S = Wide<D>;
@@ -722,7 +736,11 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   e = cudaGetLastError();
   if (e == cudaSuccess && k.narrow) e = stream(k, stream_work, st, true);
   if (e != cudaSuccess) return e;
-  return launch_after(join_wide_kernel<D>, dim3(grid, W_ROWS / J_ROWS), J_ROWS * D / 4, 0, st, a);
+  constexpr int RT = wide_row_tile(D), CTAS = W_ROWS * (D / 4) / J_THREADS;
+  const int parts = k.narrow && !whole_tiles(k.c) ? parts_of(k.c, RT) : 0;
+  const Join* join = static_cast<const Join*>(stream_work);
+  return launch_after(join_wide_kernel<D>, dim3(grid * CTAS + parts * join_ctas(RT)), J_THREADS, 0, st, a, join,
+                      reinterpret_cast<const float*>(join + parts), grid, parts);
 }
 
 static inline cudaError_t wide(const Call& k, void* work, void* stream_work, cudaStream_t st) {

@@ -699,16 +699,41 @@ __device__ __forceinline__ void join_item(const Call& k, int part_x, int row0) {
 
 // Joins the items of the wide kernel and the tiles of the streaming kernel that
 // followed it, in one launch: first `parts` CTAs for every J_THREADS threads of
-// an item, then `narrow_parts` for every join_ctas of a tile (0: none is cut).
+// an item, then CTAs that list the cut tiles among `narrow_parts` and take the
+// join_ctas shares of each in turn (a CTA per share of every part would be 2368
+// CTAs, nearly all of them empty).
 template <int D>
 __global__ void __launch_bounds__(J_THREADS) join_wide_kernel(const Call k, const Join* narrow, const float* narrow_part,
                                                               int parts, int narrow_parts) {
   constexpr int ROWS = J_THREADS / (D / 4), CTAS = W_ROWS / ROWS;
   static_assert(CTAS * ROWS == W_ROWS, "every row of an item has its threads");
   pdl_wait();
-  const int b = blockIdx.x, x = b - parts * CTAS;
-  if (x < 0) join_item<D>(k, b % parts, b / parts * ROWS);
-  else join_tile<D, wide_row_tile(D)>(k, narrow, narrow_part, x % narrow_parts, x / narrow_parts);
+  const int b = blockIdx.x;
+  if (b < parts * CTAS) {
+    join_item<D>(k, b % parts, b / parts * ROWS);
+    return;
+  }
+  extern __shared__ int s_cut[];  // [narrow_parts]
+  __shared__ int s_count[J_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int count = 0;
+  for (int i0 = 0; i0 < narrow_parts; i0 += J_THREADS) {
+    const int i = i0 + threadIdx.x;
+    const bool cut = i < narrow_parts && narrow[i].parts > 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) s_count[warp] = __popc(mask);
+    __syncthreads();
+    int at = count + __popc(mask & ((1u << lane) - 1));
+    for (int w = 0; w < J_WARPS; ++w) {
+      if (w < warp) at += s_count[w];
+      count += s_count[w];
+    }
+    if (cut) s_cut[at] = i;
+    __syncthreads();
+  }
+  constexpr int RT = wide_row_tile(D);
+  for (int u = b - parts * CTAS; u < count * join_ctas(RT); u += gridDim.x - parts * CTAS)
+    join_tile<D, RT>(k, narrow, narrow_part, s_cut[u / join_ctas(RT)], u % join_ctas(RT));
 }
 
 static inline size_t wide_workspace_bytes(const Cache& c) {
@@ -739,7 +764,7 @@ static inline cudaError_t wide_launch(const Call& k, void* work, void* stream_wo
   constexpr int RT = wide_row_tile(D), CTAS = W_ROWS * (D / 4) / J_THREADS;
   const int parts = k.narrow && !whole_tiles(k.c) ? parts_of(k.c, RT) : 0;
   const Join* join = static_cast<const Join*>(stream_work);
-  return launch_after(join_wide_kernel<D>, dim3(grid * CTAS + parts * join_ctas(RT)), J_THREADS, 0, st, a, join,
+  return launch_after(join_wide_kernel<D>, dim3(grid * CTAS + parts), J_THREADS, parts * sizeof(int), st, a, join,
                       reinterpret_cast<const float*>(join + parts), grid, parts);
 }
 

@@ -296,6 +296,19 @@ def test_attention_long(fmt, d):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_prompts_and_cut_tiles(fmt, d):
+    """Prompts and few rows in one call, both cut over the tokens: joined together."""
+    p = Pair(fmt, kvh=2, d=d, ps=64, num_pages=260, max_pages=80)
+    p.append([2, 1, 4, 0], [5001, 300, 4100, 2077])
+    p.append([2], [60], size=3.0)
+    p.attention([2, 1, 4, 0], [60, 1, 150, 9], group=1, pad=1)
+    p.attention([4, 0, 2], [33, 7, 1], group=2)
+    p.attention([0, 2, 4], [0, 3, 1], group=3, max_q=500)  # few rows where max_q allows a prompt
+    p.attention([2], [2], group=1, max_q=500)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("room", [32, 256])
 def test_attention_scales_far_apart(fmt, room):
     """Pages whose values differ by many powers of two, scores far apart and

@@ -321,6 +321,8 @@ static inline Work work_of(void* w, int n, int num_pages) {
   k.rank = k.high + num_pages;
   return k;
 }
+// where a resize or fork with this workspace leaves whether it went through (0: refused)
+static inline const int32_t* go_word(const void* w) { return static_cast<const int32_t*>(w); }
 static inline size_t workspace_bytes(int n, int num_pages) { return 4 * (HEAD + 3 * (size_t)n + 3 * (size_t)num_pages); }
 
 // exclusive prefix sum over the block; `total` receives the sum

@@ -239,25 +239,26 @@ __global__ void __launch_bounds__(SAMPLE_THREADS) sample_kernel(const bf16* __re
 
 // Before a paged step's resize: row b's token goes to the slot's position
 // lens[slot], or, for a prefill, T0 tokens to 0 .. T0 - 1.  A slot out of range
-// or without room (P positions) asks for the length -1, which refuses the call.
+// or without room (P positions) asks for the length -1, which refuses the call,
+// and so does every slot of a prefill whose freeing resize was refused (freed,
+// the word that a resize leaves in its workspace; NULL for a step).
 __global__ void paged_before_kernel(const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int num_slots,
-                                    int P, int B, int T0, int32_t* __restrict__ pos, int32_t* __restrict__ new_len) {
+                                    int P, int B, int T0, const int32_t* __restrict__ freed, int32_t* __restrict__ pos,
+                                    int32_t* __restrict__ new_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
   const int slot = slots[b];
   const int len = T0 > 0 ? 0 : (unsigned)slot < (unsigned)num_slots ? lens[slot] : P;
   const int after = len + (T0 > 0 ? T0 : 1);
-  pos[b] = after <= P ? after - 1 : 0;
-  new_len[b] = after <= P ? after : -1;
+  const bool ok = after <= P && (freed == nullptr || *freed != 0);
+  pos[b] = ok ? after - 1 : 0;
+  new_len[b] = ok ? after : -1;
 }
 // After it: the row offsets of append and attention, all 0 (no rows) when the
-// resize was refused, so that the cache stays as it was.
-__global__ void paged_after_kernel(const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int num_slots,
-                                   int B, int rows, const int32_t* __restrict__ new_len, int32_t* __restrict__ cu) {
-  bool ok = true;
-  for (int b = threadIdx.x; b < B; b += blockDim.x)
-    ok &= (unsigned)slots[b] < (unsigned)num_slots && lens[slots[b]] == new_len[b];
-  ok = __syncthreads_and(ok);
+// resize was refused (resized, its word), so that the cache stays as it was.
+// (The lengths do not tell: slots of a refused prefill may hold T0 tokens already.)
+__global__ void paged_after_kernel(int B, int rows, const int32_t* __restrict__ resized, int32_t* __restrict__ cu) {
+  const bool ok = *resized != 0;
   for (int b = threadIdx.x; b <= B; b += blockDim.x) cu[b] = ok ? b * rows : 0;
 }
 
@@ -410,15 +411,16 @@ static int paged_check(gpt2* h, const gpt2_kv8* cache, kv8::Cache& c, const int3
   return GPT2_OK;
 }
 
-// The slots' lengths for T0 new tokens from position 0 (T0 > 0) or one more,
-// and the row offsets (none when refused).
+// The slots' lengths for T0 new tokens from position 0 (T0 > 0: behind the
+// resize that freed them) or one more, and the row offsets (none when refused).
 static int paged_room(gpt2* h, const kv8::Cache& c, const int32_t* slots, int B, int T0) {
-  gen::paged_before_kernel<<<(B + 255) / 256, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, h->P, B, T0, h->pg_pos,
-                                                                  h->pg_len);
+  const int32_t* go = kv8::go_word(h->pg_work);
+  gen::paged_before_kernel<<<(B + 255) / 256, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, h->P, B, T0,
+                                                                  T0 > 0 ? go : nullptr, h->pg_pos, h->pg_len);
   LAUNCH_CHECK(h);
   CU_CHECK(h, kv8::resize(c, slots, h->pg_len, B, h->pg_work, h->stream));
   h->launches += 2;
-  gen::paged_after_kernel<<<1, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, B, T0 > 0 ? T0 : 1, h->pg_len, h->pg_cu);
+  gen::paged_after_kernel<<<1, 256, 0, h->stream>>>(B, T0 > 0 ? T0 : 1, go, h->pg_cu);
   LAUNCH_CHECK(h);
   return GPT2_OK;
 }

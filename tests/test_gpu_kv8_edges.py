@@ -1,0 +1,64 @@
+"""The paged 8-bit cache where a call is refused, a page is shared or bad, or
+what a row must not see is extreme; through the C ABI against the 64-bit form
+in tests/kv8_reference.py."""
+import numpy as np
+import pytest
+
+from tests import kv8_reference as R
+from tests.gpu_util import bf16_round, need_gpu, torch
+from tests.test_gpu_kv8 import FMTS, Pair, _i32
+from tests.test_gpu_kv8_generate import Run, _dev
+
+pytestmark = pytest.mark.gpu
+
+
+def _state(c):
+    return [t.clone() for t in (c.codes.view(torch.uint8), c.scales.view(torch.int32), c.table, c.lens, c.refs)]
+
+
+def _unchanged(c, before):
+    return all(torch.equal(a, b) for a, b in zip(before, _state(c)))
+
+
+def _refused(G, call, name="ECACHE"):
+    call()
+    with pytest.raises(G.GPT2Error) as e:
+        G.check_device_error()
+    assert e.value.name == name
+
+
+# ------------------------------------------------------------ refused prefills
+@pytest.mark.parametrize("slots", [[3, 3], [3, 1, 3], [3, 8], [-1, 3]])
+def test_refused_prefill_leaves_slots_of_the_same_length(slots):
+    """A slot named twice, or one that does not exist, beside slots that hold as
+    many tokens as the call brings, their page shared with a fork."""
+    r = Run(R.INT8)
+    rng = np.random.default_rng(1)
+    r.prefill([3, 1], rng.integers(0, 500, (2, 16)))
+    r.cache.fork(_dev([3]), _dev([6]), r.work)
+    before = _state(r.cache)
+    out = torch.empty(len(slots), dtype=torch.int32, device="cuda")
+    r.m.kv8_prefill(r.cache, _dev(slots), _dev(rng.integers(0, 500, (len(slots), 16))), out)
+    with pytest.raises(r.G.GPT2Error) as e:
+        r.m.get_decode_logits(len(slots))
+    assert e.value.name == "ECACHE"
+    assert _unchanged(r.cache, before)
+    r.m.close()
+
+
+def test_prefill_without_room_has_freed_its_slots():
+    """Six pages of four: the freeing went through, and no row is written."""
+    r = Run(R.E4M3, num_pages=4, max_T=40)
+    rng = np.random.default_rng(2)
+    r.prefill([0, 1], rng.integers(0, 500, (2, 17)))
+    codes, scales = r.cache.codes.view(torch.uint8).clone(), r.cache.scales.clone()
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    r.m.kv8_prefill(r.cache, _dev([0, 1]), _dev(rng.integers(0, 500, (2, 40))), out)
+    with pytest.raises(r.G.GPT2Error) as e:
+        r.m.get_decode_logits(2)
+    assert e.value.name == "ECACHE"
+    assert torch.all(r.cache.lens == 0) and torch.all(r.cache.refs == 0)
+    assert torch.equal(codes, r.cache.codes.view(torch.uint8)) and torch.equal(scales, r.cache.scales)
+    r.ref.resize([0, 1], [0, 0])
+    r.prefill([0, 1], rng.integers(0, 500, (2, 20)))
+    r.m.close()

@@ -238,21 +238,20 @@ __global__ void __launch_bounds__(SAMPLE_THREADS) sample_kernel(const bf16* __re
 }
 
 // Before a paged step's resize: row b's token goes to the slot's position
-// lens[slot], or, for a prefill, T0 tokens to 0 .. T0 - 1.  A slot out of range
-// or without room (P positions) asks for the length -1, which refuses the call,
-// and so does every slot of a prefill whose freeing resize was refused (freed,
-// the word that a resize leaves in its workspace; NULL for a step).
-__global__ void paged_before_kernel(const int32_t* __restrict__ slots, const int32_t* __restrict__ lens, int num_slots,
-                                    int P, int B, int T0, const int32_t* __restrict__ freed, int32_t* __restrict__ pos,
+// lens[slot], or, for a prefill, T0 <= P tokens to 0 .. T0 - 1.  A slot or length
+// out of range, or without room (P positions), asks for the length -1, which
+// refuses the call, and so does every slot of a prefill whose freeing resize
+// was refused (freed, the word that a resize leaves in its workspace).  The
+// position is in 0 .. P - 1 in any case: the embedding reads it.
+__global__ void paged_before_kernel(kv8::Cache c, const int32_t* __restrict__ slots, int P, int B, int T0,
+                                    const int32_t* __restrict__ freed, int32_t* __restrict__ pos,
                                     int32_t* __restrict__ new_len) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
-  const int slot = slots[b];
-  const int len = T0 > 0 ? 0 : (unsigned)slot < (unsigned)num_slots ? lens[slot] : P;
-  const int after = len + (T0 > 0 ? T0 : 1);
-  const bool ok = after <= P && (freed == nullptr || *freed != 0);
-  pos[b] = ok ? after - 1 : 0;
-  new_len[b] = ok ? after : -1;
+  const int len = T0 > 0 ? T0 - 1 : c.len_of(slots[b]);  // -1: out of range
+  const bool ok = len >= 0 && len < P && (T0 <= 0 || *freed != 0);
+  pos[b] = ok ? len : 0;
+  new_len[b] = ok ? len + 1 : -1;
 }
 // After it: the row offsets of append and attention, all 0 (no rows) when the
 // resize was refused (resized, its word), so that the cache stays as it was.
@@ -415,8 +414,7 @@ static int paged_check(gpt2* h, const gpt2_kv8* cache, kv8::Cache& c, const int3
 // resize that freed them) or one more, and the row offsets (none when refused).
 static int paged_room(gpt2* h, const kv8::Cache& c, const int32_t* slots, int B, int T0) {
   const int32_t* go = kv8::go_word(h->pg_work);
-  gen::paged_before_kernel<<<(B + 255) / 256, 256, 0, h->stream>>>(slots, c.lens, c.num_slots, h->P, B, T0,
-                                                                  T0 > 0 ? go : nullptr, h->pg_pos, h->pg_len);
+  gen::paged_before_kernel<<<(B + 255) / 256, 256, 0, h->stream>>>(c, slots, h->P, B, T0, go, h->pg_pos, h->pg_len);
   LAUNCH_CHECK(h);
   CU_CHECK(h, kv8::resize(c, slots, h->pg_len, B, h->pg_work, h->stream));
   h->launches += 2;

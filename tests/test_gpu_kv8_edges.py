@@ -62,3 +62,27 @@ def test_prefill_without_room_has_freed_its_slots():
     r.ref.resize([0, 1], [0, 0])
     r.prefill([0, 1], rng.integers(0, 500, (2, 20)))
     r.m.close()
+
+
+@pytest.mark.parametrize("length", [-1, -5, -2 ** 31, 2 ** 31 - 1, 64, 65])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_model_calls_refuse_a_bad_stored_length(length, prefill):
+    """A length below zero, or one at which there is no next position, in the
+    caller's d_lens: refused, nothing written, no position formed from it."""
+    if prefill and length == 64:
+        return  # a full slot may be replaced
+    r = Run(R.INT8)
+    rng = np.random.default_rng(3)
+    r.prefill([3, 1], rng.integers(0, 500, (2, 16)))
+    r.cache.lens[3] = length
+    before = _state(r.cache)
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    if prefill:
+        r.m.kv8_prefill(r.cache, _dev([1, 3]), _dev(rng.integers(0, 500, (2, 16))), out)
+    else:
+        r.m.kv8_decode_step(r.cache, _dev([1, 3]), _dev([5, 6]), out)
+    with pytest.raises(r.G.GPT2Error) as e:
+        r.m.get_decode_logits(2)
+    assert e.value.name == "ECACHE"
+    assert _unchanged(r.cache, before)
+    r.m.close()

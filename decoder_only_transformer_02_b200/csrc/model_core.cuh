@@ -120,6 +120,7 @@ struct gpt2 {
   int32_t *pg_pos = nullptr, *pg_len = nullptr, *pg_cu = nullptr;
   uint8_t* pg_work = nullptr;
   size_t pg_work_bytes = 0;
+  uint8_t* pg_old[64] = {};  // earlier blocks (each at most half the next one's size)
   const int32_t* last_tok = nullptr;
   const int32_t* last_tgt = nullptr;
 
@@ -259,6 +260,8 @@ static void free_all(gpt2* h) {
                   h->tgt_dev, h->ce_part, h->attn_ds, h->kv, h->dec_x, h->dec_mean, h->dec_rstd, h->dec_ln,
                   h->dec_qkv, h->dec_att, h->dec_u, h->dec_a, h->dec_logits, h->pg_pos, h->pg_len, h->pg_cu, h->pg_work};
   for (void* p : ptrs)
+    if (p) cudaFree(p);
+  for (void* p : h->pg_old)
     if (p) cudaFree(p);
 }
 

@@ -385,7 +385,31 @@ static int decode_impl(gpt2* h, const int32_t* tok, int B, int pos, float temper
 }
 
 // ------------------------------------------------ on a paged 8-bit cache
-// Checks of both calls, and scratch for `max_q` new tokens of B sequences.
+// Scratch of the cache calls, for max_B rows.  A larger pool needs more: a new
+// block, at least twice the old one's size so that there are few of them; the
+// old one stays until the handle is destroyed, since graphs captured with it
+// may be replayed.
+static int paged_scratch(gpt2* h, const kv8::Cache& c) {
+  const int B = h->maxB < kv8::MAX_SEQS ? h->maxB : kv8::MAX_SEQS;
+  const size_t a = kv8::workspace_bytes(B, c.num_pages), b = kv8::attention_workspace_bytes(c, h->H, B, B, 1);
+  const size_t need = a > b ? a : b;
+  if (need <= h->pg_work_bytes) return GPT2_OK;
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(h->stream, &capturing) != cudaSuccess) cudaGetLastError();
+  if (capturing != cudaStreamCaptureStatusNone)
+    return set_err(h, GPT2_ESTATE, "a larger cache than before needs a call outside the capture first");
+  int k = 0;
+  while (h->pg_old[k] != nullptr) ++k;
+  uint8_t* p = nullptr;
+  const size_t bytes = need > 2 * h->pg_work_bytes ? need : 2 * h->pg_work_bytes;
+  ALLOC(h, p, bytes);
+  h->pg_old[k] = h->pg_work;
+  h->pg_work = p;
+  h->pg_work_bytes = bytes;
+  return GPT2_OK;
+}
+
+// Checks of both calls.
 static int paged_check(gpt2* h, const gpt2_kv8* cache, kv8::Cache& c, const int32_t* slots, const int32_t* tok, int B,
                        float temperature, int top_k, int32_t* d_next) {
   RET_IF(gen_check(h, temperature, top_k, d_next));
@@ -395,19 +419,7 @@ static int paged_check(gpt2* h, const gpt2_kv8* cache, kv8::Cache& c, const int3
   if (c.L != h->L || c.kvh != h->H || c.d != h->C / h->H)
     return set_err(h, GPT2_EINVAL, "the cache has other layers, heads or head dimension than the model");
   if (B > kv8::MAX_SEQS) return set_err(h, GPT2_EINVAL, "more rows than a cache call takes");
-  const size_t a = kv8::workspace_bytes(B, c.num_pages), b = kv8::attention_workspace_bytes(c, h->H, B, B, 1);
-  const size_t need = a > b ? a : b;
-  if (need > h->pg_work_bytes) {
-    CU_CHECK(h, cudaStreamSynchronize(h->stream));
-    for (size_t i = 0; h->pg_work && i < h->guards.size(); ++i)
-      if (h->guards[i].first == h->pg_work) h->guards.erase(h->guards.begin() + i);
-    if (h->pg_work) cudaFree(h->pg_work);
-    h->pg_work = nullptr;
-    h->pg_work_bytes = 0;
-    ALLOC(h, h->pg_work, need);
-    h->pg_work_bytes = need;
-  }
-  return GPT2_OK;
+  return paged_scratch(h, c);
 }
 
 // The slots' lengths for T0 new tokens from position 0 (T0 > 0: behind the

@@ -347,7 +347,10 @@ int gpt2_kv8_attention(const gpt2_kv8* cache, int layer, const void* d_q, int64_
  * head_dim 64.  Row b of a call works on slot d_slots[b] (device int32 [B],
  * distinct); the draw for its token at position p uses the slot in the place
  * of the sequence's number: splitmix64(seed * 2^32 + p * 2^16 + slot).  The
- * first call allocates the step's buffers.  A call that the cache refuses
+ * first call allocates the step's buffers, and the first one with a larger pool
+ * than any before it allocates again (GPT2_ESTATE inside a stream capture, with
+ * nothing enqueued); what was allocated stays until gpt2_destroy, so graphs
+ * captured earlier can still be replayed.  A call that the cache refuses
  * (GPT2_ECACHE at the next syncing call) leaves the cache as it was, except
  * that a refused prefill has freed its slots; d_next is then meaningless.
  * Prefill: the slots are freed and hold positions 0 .. T0-1 of d_tokens

@@ -86,3 +86,55 @@ def test_model_calls_refuse_a_bad_stored_length(length, prefill):
     assert e.value.name == "ECACHE"
     assert _unchanged(r.cache, before)
     r.m.close()
+
+
+# ------------------------------------------------------------ captured and grown
+def test_a_captured_step_survives_a_larger_pool():
+    """A step captured with a small pool, then calls with a larger one and more
+    rows, which need more scratch: the graph still replays what it captured."""
+    def fresh():
+        r = Run(R.INT8)
+        rng = np.random.default_rng(9)
+        prompts = _dev(rng.integers(0, 500, (2, 16)))
+        slots, out = _dev([3, 1]), torch.empty(2, dtype=torch.int32, device="cuda")
+        side = torch.cuda.Stream()
+        r.m.set_stream(side)
+        torch.cuda.synchronize()
+        r.m.kv8_prefill(r.cache, slots, prompts, out)
+        torch.cuda.synchronize()
+        return r, slots, out, side
+
+    eager, slots, out, _ = fresh()
+    want = []
+    for _ in range(4):
+        eager.m.kv8_decode_step(eager.cache, slots, out, out)
+        want.append(eager.m.get_decode_logits(2))
+    state = _state(eager.cache)
+    eager.m.close()
+
+    r, slots, out, side = fresh()
+    r.m.kv8_decode_step(r.cache, slots, out, out)  # (eager once)
+    np.testing.assert_array_equal(r.m.get_decode_logits(2), want[0])
+    big = r.G.KV8Cache.allocate(R.INT8, 2, 2, 64, 16, 400000, 8, 4)
+    s4, t4, o4 = _dev([0, 1, 2, 3]), _dev([5, 6, 7, 8]), torch.empty(4, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        r.m.kv8_decode_step(r.cache, slots, out, out)
+        with pytest.raises(r.G.GPT2Error) as e:  # more scratch is not to be had in a capture, which goes on
+            r.m.kv8_decode_step(big, s4, t4, o4)
+        assert e.value.name == "ESTATE"
+    for i in (1, 2, 3):
+        r.m.kv8_decode_step(big, s4, t4, o4)
+        torch.cuda.synchronize()
+        if i == 1:  # whatever was given back would be taken and overwritten here
+            rest = [torch.full((1 << 20,), 0x5a, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        got = r.m.get_decode_logits(4)[:2]  # (the rows of the last call that the handle knows of: four)
+        np.testing.assert_array_equal(got, want[i])
+    assert all(torch.equal(a, b) for a, b in zip(state, _state(r.cache)))
+    assert r.m.check_guards() == 0
+    del rest
+    r.m.close()

@@ -20,7 +20,7 @@ enum DeviceErr : int {
   // refused by a paged-cache kernel (GPT2_ECACHE; codes from DERR_KV8_ARGS on)
   DERR_KV8_ARGS = 16,   // a slot, length or row offset out of range, or a slot named twice
   DERR_KV8_PAGES = 17,  // not enough free pages
-  DERR_KV8_TABLE = 18,  // a page table entry outside the pool, or of a free page
+  DERR_KV8_TABLE = 18,  // a page table entry outside the pool, or (to be written) of a page that is free or shared
 };
 
 // (the library is one translation unit, so this is its single definition)

@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
     if (tid == 0) set_device_err(DERR_KV8_TABLE);
     return;
   }
+  // (looked at behind the rows' loads, which it would otherwise keep waiting)
+  const int holders = __ldcg(c.refs + page);
   const int d8 = c.d >> 3, m = end - pos;       // 16-byte pieces of a row; rows
   const int per = 32 / d8, sub = lane / d8;     // rows a warp reads at once; this lane's
   const int off = pos & (c.ps - 1);
@@ -227,6 +229,10 @@ __global__ void __launch_bounds__(32 * APPEND_WARPS)
 #pragma unroll
     for (int i = 0; i < HELD; ++i) largest(x[i]);
     mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    if (holders != 1) {  // a page that other slots read too, or that is free
+      if (lane == 0) set_device_err(DERR_KV8_TABLE);
+      return;
+    }
     uint32_t bits = scale_bits_for(mx, FMT);
     if (off != 0) {
       if (bits > old && bits != NAN_SCALE) {  // positive floats and the NaN order as their bits

@@ -317,8 +317,10 @@ int gpt2_kv8_compact(const gpt2_kv8* cache, int32_t* d_live, void* d_work, size_
  * scale (and keeps it when that token is cut off again).  Codes are rounded to
  * nearest even.  A value that is not finite makes
  * its block read as NaN.  A slot named twice (its later entries) or shorter
- * than its rows is skipped and recorded (GPT2_ECACHE); offsets that decrease
- * or pass `rows` refuse the whole call. */
+ * than its rows is skipped and recorded (GPT2_ECACHE), and so are the rows that
+ * fall into a page which another slot holds too, or none (after a fork,
+ * gpt2_kv8_resize first: new tokens then go to pages of the slot's own);
+ * offsets that decrease or pass `rows` refuse the whole call. */
 int gpt2_kv8_append(const gpt2_kv8* cache, int layer, const void* d_k, const void* d_v, int64_t ld,
                     const int32_t* d_slots, const int32_t* d_cu, int n, int rows, void* cuda_stream);
 /* Scratch of gpt2_kv8_attention with these arguments (16-byte aligned); it needs no initialisation. */

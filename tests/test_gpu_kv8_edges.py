@@ -138,3 +138,45 @@ def test_a_captured_step_survives_a_larger_pool():
     assert r.m.check_guards() == 0
     del rest
     r.m.close()
+
+
+# -------------------------------------------- append into pages of several slots
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("ps,news", [(16, 3), (16, 40), (64, 70), (128, 1)])
+def test_append_does_not_write_into_a_shared_page(fmt, ps, news):
+    """Rows that reach a page which another slot holds, or a free one, are
+    skipped and recorded; the sequence's own pages are written."""
+    p = Pair(fmt, kvh=3, ps=ps, num_pages=20)
+    p.append([0, 2], [2 * ps, 5])
+    p.fork([0], [1])
+    before = _state(p.dev)
+    x = torch.randn(news + 1, 2, 3, 64, device="cuda").bfloat16()
+
+    def put(slot):
+        p.dev.append(0, x[:, 0], x[:, 1], _i32([slot]), _i32([0, min(news, 2 * ps)]))
+
+    for slot in (0, 1):
+        _refused(p.G, lambda: put(slot))
+        assert _unchanged(p.dev, before)
+    p.resize([0], [2 * ps + 1])  # a page of its own behind the shared ones
+    m = min(news, 2 * ps)
+    before = _state(p.dev)
+    if m == 1:
+        put(0)
+        p.G.check_device_error()
+    else:
+        _refused(p.G, lambda: put(0))
+    own = int(p.dev.table[0, 2])
+    keep = torch.arange(20, device="cuda") != own
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(before[:2], _state(p.dev)[:2]))
+    k = x[m - 1:m].double().cpu().numpy()
+    p.ref.append(0, k[:, 0], k[:, 1], [0], [0, 1])
+    p.same()
+    p.dev.refs[int(p.dev.table[2, 0])] = 0  # (a count that the caller has lost)
+    before = _state(p.dev)
+    p.dev.append(0, x[:1, 0], x[:1, 1], _i32([2]), _i32([0, 1]))
+    with pytest.raises(p.G.GPT2Error):
+        p.G.check_device_error()
+    assert _unchanged(p.dev, before)
+    p.dev.refs[int(p.dev.table[2, 0])] = 1
+    p.append([0, 1, 2], [3, 4, 5])

@@ -474,7 +474,7 @@ static int paged_decode_impl(gpt2* h, const gpt2_kv8* cache, const int32_t* slot
     CU_CHECK(h, kv8::append(c, l, h->dec_qkv + C, h->dec_qkv + 2 * C, 3L * C, slots, h->pg_cu, B, B, h->stream));
     CU_CHECK(h, kv8::attention(c, l, h->dec_qkv, 3L * C, h->dec_att, C, nullptr, h->H, slots, h->pg_cu, B, B, 1, h->pg_work,
                                h->stream));
-    h->launches += 3;
+    h->launches += kv8::whole_tiles(c) ? 2 : 3;  // (whole tiles need no join)
     return GPT2_OK;
   }));
   return gen_sample(h, h->dec_logits, h->Vp, B, temperature, top_k, seed, 0, h->pg_pos, slots, d_next);

@@ -180,3 +180,45 @@ def test_append_does_not_write_into_a_shared_page(fmt, ps, news):
     assert _unchanged(p.dev, before)
     p.dev.refs[int(p.dev.table[2, 0])] = 1
     p.append([0, 1, 2], [3, 4, 5])
+
+
+def _kernels_of(graph):
+    """Kernel nodes of a captured graph."""
+    from cuda.bindings import runtime as rt
+
+    def ok(r):
+        assert r[0] == rt.cudaError_t.cudaSuccess, r[0]
+        return r[1:]
+
+    raw = rt.cudaGraph_t(graph.raw_cuda_graph())
+    n = ok(rt.cudaGraphGetNodes(raw, 0))[-1]
+    nodes = ok(rt.cudaGraphGetNodes(raw, n))[0]
+    return sum(ok(rt.cudaGraphNodeGetType(x))[0] == rt.cudaGraphNodeType.cudaGraphNodeTypeKernel for x in nodes[:n])
+
+
+@pytest.mark.parametrize("max_pages", [4, 256])  # whole tiles, or cut ones that are joined
+@pytest.mark.parametrize("prefill", [False, True])
+def test_launches_are_counted(max_pages, prefill):
+    r = Run(R.INT8)
+    cache = r.G.KV8Cache.allocate(R.INT8, 2, 2, 64, 16, 40, 8, max_pages)
+    side = torch.cuda.Stream()
+    r.m.set_stream(side)
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    slots, tokens, prompt = _dev([2, 5]), _dev([7, 9]), _dev(np.ones((2, 16)))
+    torch.cuda.synchronize()
+
+    def call():
+        if prefill:
+            r.m.kv8_prefill(cache, slots, prompt, out)
+        else:
+            r.m.kv8_decode_step(cache, slots, tokens, out)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph, stream=side):
+        n = r.m.kernel_launches
+        call()
+        n = r.m.kernel_launches - n
+    assert n == _kernels_of(graph)
+    r.m.close()

@@ -12,21 +12,23 @@ typedef __nv_bfloat16 bf16;
 // Library-wide device error word.  Kernels never trap: a bounded wait that
 // gives up, or an out-of-range index, records a code here and the kernel
 // returns.  The host reads and clears it at its sync points.
+// Of several codes the highest stays: a call that the paged cache refused must
+// not hide a wait that gave up, whose kernel left its outputs incomplete.
 enum DeviceErr : int {
   DERR_NONE = 0,
-  DERR_TOKEN_RANGE = 1,     // a token or target id >= padded vocab
-  DERR_WAIT_TIMEOUT = 2,    // an mbarrier wait ran past its limit
-  DERR_NONFINITE = 3,       // non-finite gradient norm (update skipped)
-  // refused by a paged-cache kernel (GPT2_ECACHE; codes from DERR_KV8_ARGS on)
-  DERR_KV8_ARGS = 16,   // a slot, length or row offset out of range, or a slot named twice
-  DERR_KV8_PAGES = 17,  // not enough free pages
-  DERR_KV8_TABLE = 18,  // a page table entry outside the pool, or (to be written) of a page that is free or shared
+  // refused by a paged-cache kernel (GPT2_ECACHE; codes up to DERR_KV8_TABLE)
+  DERR_KV8_ARGS = 1,   // a slot, length or row offset out of range, or a slot named twice
+  DERR_KV8_PAGES = 2,  // not enough free pages
+  DERR_KV8_TABLE = 3,  // a page table entry outside the pool, or (to be written) of a page that is free or shared
+  DERR_TOKEN_RANGE = 16,   // a token or target id >= padded vocab
+  DERR_WAIT_TIMEOUT = 17,  // an mbarrier wait ran past its limit
+  DERR_NONFINITE = 18,     // non-finite gradient norm (update skipped)
 };
 
 // (the library is one translation unit, so this is its single definition)
 __device__ int g_device_err = 0;
 
-__device__ __forceinline__ void set_device_err(int code) { atomicCAS(&g_device_err, 0, code); }
+__device__ __forceinline__ void set_device_err(int code) { atomicMax(&g_device_err, code); }
 
 // Time after which a pipeline wait (a warp waiting for its producer or
 // consumer) gives up, in nanoseconds of %globaltimer.  Settable from the host

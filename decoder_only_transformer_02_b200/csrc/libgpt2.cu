@@ -497,7 +497,7 @@ int gpt2_check_device_error(void* stream) {
   if (derr == 0) return GPT2_OK;
   const int zero = 0;
   if (cudaMemcpyToSymbol(g_device_err, &zero, sizeof(int)) != cudaSuccess) cudaGetLastError();
-  return derr >= DERR_KV8_ARGS ? GPT2_ECACHE : GPT2_ECUDA;
+  return derr <= DERR_KV8_TABLE ? GPT2_ECACHE : GPT2_ECUDA;
 }
 
 int gpt2_set_wait_limit_ns(uint64_t limit_ns) {

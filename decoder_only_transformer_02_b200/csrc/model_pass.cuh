@@ -243,7 +243,7 @@ static int check_device_flags(gpt2* h) {
   if (derr) {
     int zero = 0;
     cudaMemcpyToSymbol(g_device_err, &zero, 4);
-    if (derr >= DERR_KV8_ARGS)
+    if (derr <= DERR_KV8_TABLE)
       return set_err(h, GPT2_ECACHE, derr == DERR_KV8_PAGES   ? "not enough free cache pages"
                                      : derr == DERR_KV8_TABLE ? "a page table entry is outside the cache, or names a free or shared page"
                                                               : "a cache slot, length or row offset is out of range");

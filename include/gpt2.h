@@ -376,8 +376,8 @@ int gpt2_kv8_decode_step(gpt2_t* h, const gpt2_kv8* cache, const int32_t* d_slot
  * gpt2_check_device_error synchronises cuda_stream (NULL = legacy default
  * stream), then reads and clears the error word of the current device.
  * Returns GPT2_OK when no kernel recorded an error since the last check,
- * GPT2_ECACHE when a paged-cache call was refused on the device, and
- * GPT2_ECUDA otherwise (or when the synchronisation failed).  The word is shared
+ * GPT2_ECACHE when paged-cache calls were refused on the device, and
+ * GPT2_ECUDA otherwise (also when both happened, or the synchronisation failed).  The word is shared
  * by every caller on the device: check before trusting a standalone result. */
 int gpt2_check_device_error(void* cuda_stream);
 /* Testing support: the time after which a device-side pipeline wait gives up,

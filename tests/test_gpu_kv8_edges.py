@@ -222,3 +222,26 @@ def test_launches_are_counted(max_pages, prefill):
         n = r.m.kernel_launches - n
     assert n == _kernels_of(graph)
     r.m.close()
+
+
+def test_a_refused_call_does_not_hide_a_wait_that_gave_up():
+    """A refusal first, then a prompt whose waits run out: what is incomplete is reported."""
+    p = Pair(R.INT8, kvh=2, ps=32, num_pages=60, max_pages=40)
+    p.append([0, 1], [900, 500])
+    work = torch.empty(p.dev.attention_workspace_bytes(2, 2, 1000, 700), dtype=torch.uint8, device="cuda")
+    q = torch.randn(1000, 2, 64, device="cuda").bfloat16()
+    out = torch.zeros_like(q)
+    for first in (True, False):
+        try:
+            p.G.set_wait_limit_ns(1)
+            if first:
+                p.dev.resize(_i32([0, 0]), _i32([1, 1]), p.work)
+            p.dev.attention(0, q, out, _i32([0, 1]), _i32([0, 700, 1000]), 700, work)
+            if not first:
+                p.dev.resize(_i32([0, 0]), _i32([1, 1]), p.work)
+            with pytest.raises(p.G.GPT2Error) as e:
+                p.G.check_device_error()
+            assert e.value.name == "ECUDA"
+        finally:
+            p.G.set_wait_limit_ns(0)
+        p.G.check_device_error()

@@ -347,20 +347,21 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
           if (!(vsc <= 3.0e38f)) ksc = vsc;  // a block that is not a number is none for the scores either
         } else {
           set_device_err(DERR_KV8_TABLE);
-          pg = 0;
+          pg = -1;
           ksc = vsc = __uint_as_float(NAN_SCALE);
         }
       }
     };
-    // starts the copies of a step; keys and values of tokens behind the last become zero
+    // starts the copies of a step; keys and values of tokens behind the last become zero, and those of a page
+    // outside the pool (what would be read in its place may be no numbers, which a weight of 0 does not hide)
     auto load = [&](int step, int stage) {
       const int gi = own + step * (W * U), at = (step - base) * U;
       const uint32_t dst = ring + stage * S::STEP;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int page = __shfl_sync(0xffffffffu, pg, at + u);
-        const uint8_t* t = head_base + page * page_stride + (((gi + u) << 4) & (c.ps - 1)) * D;
-        const int left = gi + u < p.g1 ? p.e.len - (gi + u) * GROUP : 0;
+        const uint8_t* t = head_base + max(page, 0) * page_stride + (((gi + u) << 4) & (c.ps - 1)) * D;
+        const int left = gi + u < p.g1 && page >= 0 ? p.e.len - (gi + u) * GROUP : 0;
 #pragma unroll
         for (int r = 0; r < GROUP; r += ROWS) {
           const int row = r + crow, tok = sigma(row);

@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           const int s = g % NS;
           // factors of the block's pages
           if (bad) set_device_err(DERR_KV8_TABLE);
+          const uint32_t bads = __ballot_sync(0xffffffffu, bad);  // pages whose codes are not the sequence's
           const bool nan = bad || !(ks <= 3.0e38f && vs <= 3.0e38f);
           const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(ks)))));
           const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(vs)))));
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
                 const int row0 = (i & (PER_SIDE - 1)) * ROWS;
                 const uint32_t f = __shfl_sync(0xffffffffu, side ? vf : kf, row0 >> c.ps_log2);
                 uint4 w = cur[e];
-                if (left < W_KEYS && row0 + lrow >= left) w = make_uint4(0, 0, 0, 0);
+                if ((left < W_KEYS && row0 + lrow >= left) || (bads >> (row0 >> c.ps_log2) & 1u)) w = make_uint4(0, 0, 0, 0);
                 uint32_t x[8];
                 codes16_half<FMT>(w, f, x);
                 const uint32_t to = smem_u32(smem + S::KV_OFF + (2 * s + side) * S::TILE) + (row0 >> 3) * 1024 + lane_to;

@@ -245,3 +245,63 @@ def test_a_refused_call_does_not_hide_a_wait_that_gave_up():
         finally:
             p.G.set_wait_limit_ns(0)
         p.G.check_device_error()
+
+
+# ------------------------------------------------------------------- bad pages
+def _near(p, slot, q, out, lse, first):
+    """The rows of `slot` (its last ones) before position `first` against the
+    64-bit form; tolerances as in tests/test_gpu_kv8.py, with the largest value
+    taken over the tokens before `first` alone.  Returns which rows those are."""
+    rows, heads, d = q.shape
+    n = int(p.ref.lens[slot])
+    blind = np.arange(n - rows, n) < first
+    assert blind.any() and not blind.all()
+    m = int(blind.sum())
+    want, wl, mag, top = p.ref.attention(0, q.double().cpu().numpy(), [slot], [0, rows])
+    ds = 2 * d * 2.0 ** -24 * top[:m]
+    v = np.abs(p.ref.values(0, slot)[1][:first]).max((0, 2)).repeat(heads // p.ref.kvh)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14) * mag + 2.0 ** -30 * first * v[:, None]
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.all(np.abs(got - want)[:m] <= bound[:m] + 2 * ds[..., None] * mag[:m])
+    assert np.all(np.abs(gl - wl)[:m] <= ds + 2.0 ** -20 * (1 + np.abs(wl[:m])))
+    return torch.from_numpy(blind).cuda()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,ps", [(64, 16), (64, 128), (128, 16), (128, 64)])
+@pytest.mark.parametrize("rows", [5, 200])       # the streaming kernel, the prompt kernel
+@pytest.mark.parametrize("room", [512, 8192])    # tiles whole, or cut
+def test_a_page_outside_the_pool_reaches_its_readers_only(fmt, d, ps, rows, room):
+    """Rows that see a token of it are NaN; those before it are as the
+    definition has them, and those of the other sequence, and of none, as with
+    a clean table."""
+    p = Pair(fmt, kvh=2, d=d, ps=ps, num_pages=90, max_pages=room // ps)
+    p.append([6], [3])
+    p.append([0, 1], [290, 259])
+    p.resize([6], [0])  # page 0 is free, and holds codes that are no number
+    p.dev.codes.view(torch.uint8)[0] = 0x7f
+    p.dev.scales[0] = float("nan")
+    q = torch.randn(2 * rows + 1, 4, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    work = torch.empty(p.dev.attention_workspace_bytes(4, 2, len(q), rows), dtype=torch.uint8, device="cuda")
+
+    def call():
+        out, lse = torch.full_like(q, 7.0), torch.full((len(q), 4), 7.0, device="cuda")
+        p.dev.attention(0, q, out, _i32([1, 0]), _i32([0, rows, 2 * rows]), rows, work, lse=lse)
+        return out, lse
+
+    want = call()
+    p.G.check_device_error()
+    assert torch.isfinite(want[0].float()).all()
+    kept = int(p.dev.table[1, 256 // ps])
+    for page in (-1, 90, 2 ** 31 - 1):
+        p.dev.table[1, 256 // ps] = page
+        got = call()
+        with pytest.raises(p.G.GPT2Error) as e:
+            p.G.check_device_error()
+        assert e.value.name == "ECACHE"
+        blind = _near(p, 1, q[:rows], got[0][:rows], got[1][:rows], 256)
+        for g, w in zip(got, want):
+            assert torch.isnan(g[:rows][~blind].float()).all()
+            assert torch.equal(g[rows:], w[rows:])
+    p.dev.table[1, 256 // ps] = kept
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))

@@ -23,7 +23,7 @@
 //    scaled by a power of two into f16's range (bf16 has fewer fraction bits,
 //    so this too is exact for components within 2^-29 of the row's largest).
 //  - Weights: p vs 2^6 / vref in f16 (2^-11 relative), vref the largest value
-//    scale seen, so that they stay below 2^14; sums, maxima, scores and O in fp32.
+//    scale up to the token, so that they stay below 2^14; sums, maxima, scores and O in fp32.
 //  - The row maximum moves only when a score passes it by 2^8 (one vote per
 //    step instead of a reduction over the lanes).
 //  - Each warp keeps three 4 KB steps of codes in flight (asynchronous copies
@@ -250,7 +250,10 @@ __device__ __forceinline__ int place(int row, int piece) {
 // the row of token t of a group, and the token of a row
 __device__ __forceinline__ int sigma(int t) { return t ^ ((t >> 1) & 1); }
 
-template <int FMT, int D, int NT, int W, bool SPLIT>
+// MANY: sequences may have several rows, some of which do not see all tokens of
+// a tile.  (With single rows that part of the loop, never taken, costs 0.3 us of
+// 6.4 for one sequence and 0.6 of 19.2 for 64: its instructions are fetched.)
+template <int FMT, int D, int NT, int W, bool SPLIT, bool MANY>
 __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel(const Call k) {
   using S = Shape<D, NT, W>;
   constexpr int RT = S::RT, CH = S::CH, U = S::U, VW = S::VW;
@@ -390,9 +393,13 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
     }
+    // vref: the largest value scale so far (not of NaN blocks).  A row's weights
+    // have to be held relative to what the row sees, or a later token's value could
+    // leave nothing of them: batches count the groups that every row sees, the
+    // others follow one by one.  (Rows that do not see the group that raises it
+    // have only O scaled, in fp32.)
     float vref = 0.f, vinv = 0.f;
-    auto raise = [&]() {  // vref: the largest value scale of the batches so far (not of NaN blocks)
-      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, vsc <= 3.0e38f ? __float_as_uint(fabsf(vsc)) : 0u));
+    auto raise = [&](float top) {  // (the warp's lanes agree)
       if (top > vref) {
         if (vref > 0.f) {
           const float f = vref / top;
@@ -406,6 +413,11 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         vref = top;
         vinv = 1.f / top;
       }
+    };
+    auto raise_batch = [&](int minpos) {  // the groups that begin at minpos, the first row's token, or before
+      const int gi = own + (base + lane / U) * (W * U) + lane % U;
+      const bool on = gi * GROUP <= minpos && vsc <= 3.0e38f;
+      raise(__uint_as_float(__reduce_max_sync(0xffffffffu, on ? __float_as_uint(vsc) : 0u)));
     };
     batch(0, !SPLIT);
 #pragma unroll
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
         pos[nt][j] = pos0 + (p.row0 + nt * 8 + 2 * tg + j) / k.group;
       }
     }
-    raise();
+    raise_batch(minpos);
 
     int stage = 0;
     for (int step = 0, gi = own; gi < p.g1; ++step, gi += W * U) {
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
           if (nx - base >= 32 / U) {
             batch(nx, false);
             load(nx, free_stage);
-            raise();
+            raise_batch(minpos);
           } else {
             load(nx, free_stage);
           }
@@ -567,6 +579,14 @@ __global__ void __launch_bounds__(32 * W, (Shape<D, NT, W>::CTAS)) stream_kernel
       // ---- weights, and the values' products
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (MANY && edge) {
+          float v;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(sc + 8 * u + 4));
+          if (v <= 3.0e38f) {
+            raise(v);
+            vs[u] = v * vinv * 64.f;
+          }
+        }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -763,13 +783,13 @@ static inline size_t stream_workspace_bytes(const Cache& c, int H, int max_q) {
   return (size_t)parts_of(c, rt) * (sizeof(Join) + 2 * rt * (c.d + 2) * 4);
 }
 
-template <int FMT, int D, int NT, int W, bool SPLIT>
+template <int FMT, int D, int NT, int W, bool SPLIT, bool MANY>
 static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t st, bool behind) {
   using S = Shape<D, NT, W>;
   const size_t smem = S::BYTES + (SPLIT ? Line::bytes(k.n) : 0);
   static DeviceOnce once;
   cudaError_t e = run_once_per_device(once, [] {
-    return cudaFuncSetAttribute(stream_kernel<FMT, D, NT, W, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(stream_kernel<FMT, D, NT, W, SPLIT, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 S::BYTES + (SPLIT ? (int)Line::bytes(MAX_SEQS) : 0));
   });
   if (e != cudaSuccess) return e;
@@ -777,17 +797,17 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
   if (!SPLIT) {
     const long tiles = (long)k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + S::RT - 1) / S::RT);
     const dim3 grid((unsigned)tiles, k.n);
-    if (behind) return launch_after(stream_kernel<FMT, D, NT, W, SPLIT>, grid, 32 * W, smem, st, a);
-    stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
+    if (behind) return launch_after(stream_kernel<FMT, D, NT, W, SPLIT, MANY>, grid, 32 * W, smem, st, a);
+    stream_kernel<FMT, D, NT, W, SPLIT, MANY><<<grid, 32 * W, smem, st>>>(a);
     return cudaGetLastError();
   }
   const int grid = parts_of(k.c, S::RT);
   a.join = static_cast<Join*>(work);
   a.part = reinterpret_cast<float*>(a.join + grid);
   if (behind) {
-    e = launch_after(stream_kernel<FMT, D, NT, W, SPLIT>, dim3(grid), 32 * W, smem, st, a);
+    e = launch_after(stream_kernel<FMT, D, NT, W, SPLIT, MANY>, dim3(grid), 32 * W, smem, st, a);
   } else {
-    stream_kernel<FMT, D, NT, W, SPLIT><<<grid, 32 * W, smem, st>>>(a);
+    stream_kernel<FMT, D, NT, W, SPLIT, MANY><<<grid, 32 * W, smem, st>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || behind) return e;  // (the wide kernel's join takes these tiles too)
@@ -798,19 +818,23 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
 // one sequence of 777: 6.3 (eight warps; sixteen 7.2), and cut 8.9.
 constexpr long WHOLE_TOKENS = 2048;
 static inline bool whole_tiles(const Cache& c) { return (long)c.max_pages * c.ps <= WHOLE_TOKENS; }
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, bool MANY>
 static inline cudaError_t stream_mode(const Call& k, void* work, cudaStream_t st, bool behind) {
   const long tiles = (long)k.n * k.c.kvh * ((narrow_rows((long)k.max_q * k.group) + 8 * NT - 1) / (8 * NT));
   if (whole_tiles(k.c))
-    return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false>(k, work, st, behind) : stream_launch<FMT, D, NT, 4, false>(k, work, st, behind);
-  return stream_launch<FMT, D, NT, 4, true>(k, work, st, behind);
+    return tiles <= sm_count() ? stream_launch<FMT, D, NT, 8, false, MANY>(k, work, st, behind) : stream_launch<FMT, D, NT, 4, false, MANY>(k, work, st, behind);
+  return stream_launch<FMT, D, NT, 4, true, MANY>(k, work, st, behind);
+}
+template <int FMT, int D, int NT>
+static inline cudaError_t stream_many(const Call& k, void* work, cudaStream_t st, bool behind) {
+  return k.max_q > 1 ? stream_mode<FMT, D, NT, true>(k, work, st, behind) : stream_mode<FMT, D, NT, false>(k, work, st, behind);
 }
 template <int FMT>
 static inline cudaError_t stream_rows(const Call& k, void* work, cudaStream_t st, bool behind) {
   const int rt = behind ? wide_row_tile(k.c.d) : row_tile_of(k.c, k.group, k.max_q);  // (as the join behind both has it)
   if (k.c.d == 64)
-    return rt == 8 ? stream_mode<FMT, 64, 1>(k, work, st, behind) : rt == 16 ? stream_mode<FMT, 64, 2>(k, work, st, behind) : stream_mode<FMT, 64, 4>(k, work, st, behind);
-  return rt == 8 ? stream_mode<FMT, 128, 1>(k, work, st, behind) : stream_mode<FMT, 128, 2>(k, work, st, behind);
+    return rt == 8 ? stream_many<FMT, 64, 1>(k, work, st, behind) : rt == 16 ? stream_many<FMT, 64, 2>(k, work, st, behind) : stream_many<FMT, 64, 4>(k, work, st, behind);
+  return rt == 8 ? stream_many<FMT, 128, 1>(k, work, st, behind) : stream_many<FMT, 128, 2>(k, work, st, behind);
 }
 
 // behind: it follows the wide kernel of the same call and may start before that one ends

@@ -305,3 +305,26 @@ def test_a_page_outside_the_pool_reaches_its_readers_only(fmt, d, ps, rows, room
             assert torch.equal(g[rows:], w[rows:])
     p.dev.table[1, 256 // ps] = kept
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+# ------------------------------------------------ values that a row does not see
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,ps", [(64, 16), (64, 32), (128, 16), (128, 64)])
+@pytest.mark.parametrize("rows", [30])
+@pytest.mark.parametrize("room", [512, 8192])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 40, 2.0 ** 100])
+def test_later_tokens_do_not_reach_earlier_rows(fmt, d, ps, rows, room, size):
+    """The last tokens' keys and values are `size` times the others': rows
+    before their page are held to the tokens that they see."""
+    p = Pair(fmt, kvh=2, d=d, ps=ps, num_pages=90, max_pages=room // ps)
+    p.append([0, 1], [256, 200])
+    p.append([0, 1], [17, 9], size=size)  # (slot 1: from the middle of a page on)
+    q = torch.randn(2 * rows, 4, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    out, lse = torch.zeros_like(q), torch.zeros(2 * rows, 4, device="cuda")
+    work = torch.empty(p.dev.attention_workspace_bytes(4, 2, 2 * rows, rows), dtype=torch.uint8, device="cuda")
+    p.dev.attention(0, q, out, _i32([0, 1]), _i32([0, rows, 2 * rows]), rows, work, lse=lse)
+    p.G.check_device_error()
+    for i, first in ((0, 256), (1, 192)):
+        at = slice(i * rows, (i + 1) * rows)
+        _near(p, i, q[at], out[at], lse[at], first)
+    assert torch.isfinite(out.float()).all()

@@ -13,9 +13,13 @@
 // six warps convert each block on its way: the codes of the next 16 KB are
 // loaded while these 16 KB are converted and stored as swizzled f16 tiles.  A
 // key block's values are code * scale / (the block's largest scale), exact in
-// f16 unless 2^15 or more below it; the largest scale multiplies the scores.
-// Values are taken relative to the largest scale so far; when that rises, O is
-// scaled down as it is when the row maximum moves.
+// f16 up to a ratio of 2^24 (int8) or 2^15 (e4m3); the largest scale multiplies
+// the scores.  Values are taken relative to the largest scale so far; when that
+// rises, O is scaled down as it is when the row maximum moves.
+// A block whose pages' scales may lie further apart is stored as bare codes.  The
+// softmax then multiplies a page's scores by its scale, and its weights by its
+// value scale over the largest that the row sees: what a row does not see, or
+// gives no weight, must not take the precision of what it does (far_block).
 //
 // Roles (512 threads of 128 registers, one CTA per SM): warps 0-3, 14 and 15
 // convert, warps 4-7 and 8-11 are the softmax of tile 0 and 1, warps 12 and 13
@@ -53,8 +57,9 @@ struct Wide {
   static constexpr int TILE = 128 * D * 2;               // one f16 tile: Q, K or V
   static constexpr int KV_OFF = 2 * TILE;                // after the two Q tiles; stage s: K, V
   static constexpr int BAR_OFF = KV_OFF + NS * 2 * TILE;
-  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale, value scale so far
-  static constexpr int LINE_OFF = INFO_OFF + 256;
+  static constexpr int INFO_OFF = BAR_OFF + 256;         // float2 per stage: key block scale (< 0: apart), value scale so far
+  static constexpr int APART_OFF = INFO_OFF + 256;       // float2 per stage and page of the block: key and value scale
+  static constexpr int LINE_OFF = APART_OFF + 256;
   static constexpr int UNITS = D / 64;                   // 16 KB units of codes in a block: all of it, or keys, values
   // TMEM columns of a tile: S, P (in place of S's first 64 when d = 128), O
   static constexpr uint32_t T_P = D == 64 ? 128 : 0, T_O = D == 64 ? 192 : 128;
@@ -196,8 +201,94 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// The softmax of a block whose pages' scales may lie apart (scale.x < 0), or whose
+// scores may pass 2^20 (a sum of products is below 2^30): there the fused z of the
+// common case would differ from the maximum, which is rounded, by half their last
+// place.  Rare, so the loop over the blocks is left for it and entered again: as a
+// branch in the loop it made the common case slower by a tenth (of which a twentieth
+// is left: 64 sequences of 256 over 4096 427 -> 447 us, at d = 128 679 -> 682; one
+// tile per item 346 -> 373; four chunks 61.6 -> 62.4).
+template <int D>
+__device__ __noinline__ void far_rescale(uint32_t tl, float f) {  // the row's O
+  tcg::tc_fence_after();
+#pragma unroll 1
+  for (int q = 0; q < D / 8; ++q) {
+    uint32_t o[8];
+    tmem_ld8(tl + Wide<D>::T_O + 8 * q, o);
+    tcg::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    tmem_st8(tl + Wide<D>::T_O + 8 * q, o);
+  }
+  tcfa::tmem_wait_st();
+  tcg::tc_fence_before();
+}
+struct FarRow {
+  float m, l, vref, rowf;
+};
+template <int D>
+__device__ __noinline__ bool far_block(FarRow& row, uint32_t tl, float2 scale, const volatile float2* pages, int ps_log2,
+                                       int last, uint64_t* pv_done, uint32_t phase) {
+  const bool apart = scale.x < 0.f;
+  float m = row.m, l = row.l, vref = row.vref, alpha = 1.f;
+  float vtop = apart ? vref : scale.y, mx = -INFINITY;
+  auto factor = [&](int i) { return fmaxf((apart ? pages[i * 16 >> ps_log2].x : scale.x) * row.rowf, 1e-37f); };  // of 16 tokens' scores
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    uint32_t v[16];
+    tcg::tmem_ld16(tl + 16 * i, v);
+    const float f = factor(i);
+    if (apart && 16 * i <= last) vtop = fmaxf(vtop, pages[i * 16 >> ps_log2].y);
+    tcg::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, 16 * i + e > last ? -INFINITY : __uint_as_float(v[e]) * f);
+  }
+  const bool moved = __any_sync(0xffffffffu, mx > m + 8.f);
+  const bool rescale = __any_sync(0xffffffffu, moved || vtop > vref);
+  if (moved) {
+    const float nm = fmaxf(m, mx);
+    alpha = m == -INFINITY ? 0.f : ex2_approx(m - nm);
+    m = nm;
+    l *= alpha;
+  }
+  if (vtop > vref) {
+    alpha *= vref / vtop;
+    vref = vtop;
+  }
+  const float off = m == -INFINITY ? 0.f : m - 6.f, vinv = vref > 0.f ? 1.f / vref : 0.f;
+  if (pv_done && !tcfa::warp_wait(pv_done, phase)) return false;
+  tcg::tc_fence_after();
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {  // (P's columns lie at or before those of the scores)
+    uint32_t v[16], y[8];
+    tcg::tmem_ld16(tl + 16 * i, v);
+    // a page that the row does not see may have a larger scale, but its weights are 0
+    const float f = factor(i), w = apart ? fminf(pages[i * 16 >> ps_log2].y * vinv, 1.f) : 1.f;
+    tcg::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float z0 = 16 * i + e > last ? 0.f : ex2_approx(__fmul_rn(__uint_as_float(v[e]), f) - off);
+      const float z1 = 16 * i + e + 1 > last ? 0.f : ex2_approx(__fmul_rn(__uint_as_float(v[e + 1]), f) - off);
+      l += z0 + z1;
+      y[e >> 1] = half2_of(z0 * w, z1 * w);
+    }
+    tmem_st8(tl + Wide<D>::T_P + 8 * i, y);
+  }
+  if (pv_done && rescale) far_rescale<D>(tl, alpha);
+  tcfa::tmem_wait_st();
+  tcg::tc_fence_before();
+  __syncwarp();
+  row.m = m, row.l = l, row.vref = vref;
+  return true;
 }
 
 template <int FMT, int D>
@@ -218,6 +309,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
   uint64_t* drain = pv_done + 2;                                       // 2
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   float2* info = reinterpret_cast<float2*>(smem + S::INFO_OFF);
+  float2* apart_at = reinterpret_cast<float2*>(smem + S::APART_OFF);
   long long* s_warp = reinterpret_cast<long long*>(smem + S::INFO_OFF + 128);
   long long* pre = reinterpret_cast<long long*>(smem + S::LINE_OFF);
   const Cache& c = k.c;
@@ -375,6 +467,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         bool bad = !c.page_ok(page);
         page = valid(page);
         float ks = c.scales[c.unit(page, k.layer, 0, p.head)], vs = c.scales[c.unit(page, k.layer, 1, p.head)];
+        uint32_t kexp = __shfl_sync(0xffffffffu, __float_as_uint(ks) >> 23, 0), vexp = __shfl_sync(0xffffffffu, __float_as_uint(vs) >> 23, 0);
         load(page, 0, 0);
         for (int j = p.b0; j < p.b1; ++j, ++g) {
           const int s = g % NS;
@@ -382,17 +475,24 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           if (bad) set_device_err(DERR_KV8_TABLE);
           const uint32_t bads = __ballot_sync(0xffffffffu, bad);  // pages whose codes are not the sequence's
           const bool nan = bad || !(ks <= 3.0e38f && vs <= 3.0e38f);
+          // apart: some scale more than half the exact range from what the blocks before had (so that the vote waits
+          // for no reduction)
+          constexpr int HALF = FMT == GPT2_KV_INT8 ? 12 : 7;
+          const uint32_t kd = (__float_as_uint(ks) >> 23) - kexp + HALF, vd = (__float_as_uint(vs) >> 23) - vexp + HALF;
+          const bool apart = __any_sync(0xffffffffu, !nan && max(kd, vd) > 2 * HALF);
           const float kmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(ks)))));
           const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(vs)))));
           vref = fmaxf(vref, vmax);
-          const float kr = ks * (1.f / kmax), vr = vs * (1.f / vref);
+          kexp = __float_as_uint(kmax) >> 23, vexp = __float_as_uint(vmax) >> 23;
+          const float kr = apart ? 1.f : ks * (1.f / kmax), vr = apart ? 1.f : vs * (1.f / vref);
           // a page with a scale that is not a number: its keys are not, its values 0 (only rows that see it notice)
           const uint32_t kf = nan ? 0x7e007e00u : half2_of(kr, kr), vf = nan ? 0u : half2_of(vr, vr);
           if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((g / NS) & 1u) ^ 1u))) {
             ok = false;
             break;
           }
-          if (cw == 0 && lane == 0) info[s] = make_float2(kmax, vref);
+          if (cw == 0 && lane == 0) info[s] = make_float2(apart ? -kmax : kmax, vref);
+          if (apart && cw == 0 && lane < 8) apart_at[s * 8 + lane] = nan ? make_float2(0.f, 0.f) : make_float2(ks, vs);
           const int left = p.len - j * W_KEYS;  // tokens from the block on
 #pragma unroll
           for (int u = 0; u < S::UNITS; ++u) {
@@ -489,122 +589,146 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[a]);
       }
+      // the key scale from which on a score of the warp's rows may pass 2^20 (as bits: a block apart has the sign's)
+      const uint32_t far_from = __float_as_uint(0x1p-10f / __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rowf))));
       float m = -INFINITY, l = 0.f, vref = 0.f;
       const int blocks = p.b1 - p.b0;
-      for (int j = 0; j < blocks; ++j, ++g, ++t, last -= W_KEYS, first_last -= W_KEYS) {
-        if (!warp_wait(&s_full[a], t & 1u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const volatile float2* at_info = &info[g % NS];
-        const float2 scale = make_float2(at_info->x, at_info->y);
-        const float fs = fmaxf(scale.x * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
-        const bool edge = first_last < W_KEYS - 1;
-        // The scores are read in quarters of 32; the last two twice, for the
-        // maximum and for the weights.  With all 128 kept in registers the
-        // other warps would have too few (spilled, each load would wait).
-        float mx8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
-        uint32_t x[3][32];
-        auto masked = [&](uint32_t (&v)[32], int q) {
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * q + e > last) v[e] = __float_as_uint(-INFINITY);
+      for (int j = 0; ok && j < blocks;) {
+        bool far = false;
+        for (; j < blocks; ++j, ++g, ++t, last -= W_KEYS, first_last -= W_KEYS) {
+          if (!warp_wait(&s_full[a], t & 1u)) {
+            ok = false;
+            break;
           }
-        };
-        auto maximum = [&](uint32_t (&v)[32]) {
+          tc_fence_after();
+          const volatile float2* at_info = &info[g % NS];
+          const float2 scale = make_float2(at_info->x, at_info->y);
+          const float fs = fmaxf(scale.x * rowf, 1e-37f);  // (not 0: a masked score stays -inf)
+          const bool edge = first_last < W_KEYS - 1;
+          // The scores are read in quarters of 32; the last two twice, for the
+          // maximum and for the weights.  With all 128 kept in registers the
+          // other warps would have too few (spilled, each load would wait).
+          float mx8[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float& y = mx8[(e >> 1) & 7];
-            y = fmax3(y, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          }
-        };
-        tmem_ld32(tl + 64, x[0]);
-        tmem_ld32(tl + 96, x[1]);
-        tmem_wait_ld();
-        masked(x[0], 2);
-        maximum(x[0]);
-        tmem_ld32(tl, x[0]);
-        masked(x[1], 3);
-        maximum(x[1]);
-        tmem_ld32(tl + 32, x[1]);
-        tmem_wait_ld();
-        tmem_ld32(tl + 64, x[2]);
-        masked(x[0], 0);
-        maximum(x[0]);
-        masked(x[1], 1);
-        maximum(x[1]);
-        const float mx = fs * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                    fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        // the reference moves when a row passes it by 2^8, and O also when the value scale rises
-        const bool moved = __any_sync(0xffffffffu, mx > m + 8.f);
-        const bool rescale = moved || scale.y > vref;
-        float alpha = 1.f;
-        if (moved) {
-          const float nm = fmaxf(m, mx);
-          alpha = m == -INFINITY ? 0.f : ex2f(m - nm);
-          m = nm;
-          l *= alpha;
-        }
-        if (scale.y > vref) {
-          alpha *= vref / scale.y;
-          vref = scale.y;
-        }
-        const float off = m == -INFINITY ? 0.f : m - 6.f;  // weights up to 2^14 in f16, down to 2^-30 of the reference
-        // P's place is free, and O complete, once the block before has been multiplied
-        if (j > 0 && !warp_wait(&pv_done[a], (t - 1) & 1u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 fs2 = make_float2(fs, fs), off2 = make_float2(-off, -off);
-        auto weights = [&](uint32_t (&v)[32], int q) {
+          for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
+          uint32_t x[3][32];
+          auto masked = [&](uint32_t (&v)[32], int q) {
+            if (edge) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int e = 16 * half + 2 * i;
-              float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fs2, off2);
-              z = make_float2(ex2f(z.x), ex2f(z.y));
-              sum[i & 1] = add2(sum[i & 1], z);
-              y[i] = half2_of(z.x, z.y);
+              for (int e = 0; e < 32; ++e)
+                if (32 * q + e > last) v[e] = __float_as_uint(-INFINITY);
             }
-            tmem_st8(tl + S::T_P + 16 * q + 8 * half, y);
+          };
+          auto maximum = [&](uint32_t (&v)[32]) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float& y = mx8[(e >> 1) & 7];
+              y = fmax3(y, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            }
+          };
+          tmem_ld32(tl + 64, x[0]);
+          tmem_ld32(tl + 96, x[1]);
+          tmem_wait_ld();
+          far = __float_as_uint(scale.x) > far_from;
+          if (far) break;
+          masked(x[0], 2);
+          maximum(x[0]);
+          tmem_ld32(tl, x[0]);
+          masked(x[1], 3);
+          maximum(x[1]);
+          tmem_ld32(tl + 32, x[1]);
+          tmem_wait_ld();
+          tmem_ld32(tl + 64, x[2]);
+          masked(x[0], 0);
+          maximum(x[0]);
+          masked(x[1], 1);
+          maximum(x[1]);
+          const float mx = fs * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                      fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          // the reference moves when a row passes it by 2^8, and O also when the value scale rises
+          const bool moved = __any_sync(0xffffffffu, mx > m + 8.f);
+          const bool rescale = moved || scale.y > vref;
+          float alpha = 1.f;
+          if (moved) {
+            const float nm = fmaxf(m, mx);
+            alpha = m == -INFINITY ? 0.f : ex2f(m - nm);
+            m = nm;
+            l *= alpha;
           }
-        };
-        weights(x[0], 0);
-        tmem_ld32(tl + 96, x[0]);
-        weights(x[1], 1);
-        tmem_wait_ld();
-        if (D == 64) {  // S is read: the next block's scores may be formed meanwhile
+          if (scale.y > vref) {
+            alpha *= vref / scale.y;
+            vref = scale.y;
+          }
+          const float off = m == -INFINITY ? 0.f : m - 6.f;  // weights up to 2^14 in f16, down to 2^-30 of the reference
+          // P's place is free, and O complete, once the block before has been multiplied
+          if (j > 0 && !warp_wait(&pv_done[a], (t - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 fs2 = make_float2(fs, fs), off2 = make_float2(-off, -off);
+          auto weights = [&](uint32_t (&v)[32], int q) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int e = 16 * half + 2 * i;
+                float2 z = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), fs2, off2);
+                z = make_float2(ex2f(z.x), ex2f(z.y));
+                sum[i & 1] = add2(sum[i & 1], z);
+                y[i] = half2_of(z.x, z.y);
+              }
+              tmem_st8(tl + S::T_P + 16 * q + 8 * half, y);
+            }
+          };
+          weights(x[0], 0);
+          tmem_ld32(tl + 96, x[0]);
+          weights(x[1], 1);
+          tmem_wait_ld();
+          if (D == 64) {  // S is read: the next block's scores may be formed meanwhile
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[a]);
+          }
+          masked(x[2], 2);
+          weights(x[2], 2);
+          masked(x[0], 3);
+          weights(x[0], 3);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (j > 0 && rescale) {
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tl + S::T_O + q * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tl + S::T_O + q * 32, o);
+            }
+          }
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[a]);
+          if (lane == 0) mbar_arrive(&p_full[a]);
         }
-        masked(x[2], 2);
-        weights(x[2], 2);
-        masked(x[0], 3);
-        weights(x[0], 3);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (j > 0 && rescale) {
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            tmem_ld32(tl + S::T_O + q * 32, x[0]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[0][i] = __float_as_uint(__uint_as_float(x[0][i]) * alpha);
-            tmem_st32(tl + S::T_O + q * 32, x[0]);
-          }
+        if (!far) break;
+        const volatile float2* at_info = &info[g % NS];
+        FarRow row{m, l, vref, rowf};
+        const float2 scale = make_float2(at_info->x, at_info->y);
+        ok = far_block<D>(row, tl, scale, &apart_at[(g % NS) * 8], c.ps_log2, last, j > 0 ? &pv_done[a] : nullptr, (t - 1) & 1u);
+        if (ok && lane == 0) {
+          if (D == 64) mbar_arrive(&s_free[a]);
+          mbar_arrive(&p_full[a]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[a]);
+        m = row.m, l = row.l, vref = scale.y;
+        // the rows' O to one reference again, in fp32
+        if (ok && __any_sync(0xffffffffu, row.vref != vref)) {
+          ok = warp_wait(&pv_done[a], t & 1u);
+          if (ok) far_rescale<D>(tl, row.vref / vref);
+        }
+        ++j, ++g, ++t, last -= W_KEYS, first_last -= W_KEYS;
       }
       if (!ok || !warp_wait(&pv_done[a], (t - 1) & 1u)) {
         ok = false;

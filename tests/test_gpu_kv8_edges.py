@@ -310,7 +310,7 @@ def test_a_page_outside_the_pool_reaches_its_readers_only(fmt, d, ps, rows, room
 # ------------------------------------------------ values that a row does not see
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d,ps", [(64, 16), (64, 32), (128, 16), (128, 64)])
-@pytest.mark.parametrize("rows", [30])
+@pytest.mark.parametrize("rows", [30, 100])      # the streaming kernel, the prompt kernel
 @pytest.mark.parametrize("room", [512, 8192])
 @pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 40, 2.0 ** 100])
 def test_later_tokens_do_not_reach_earlier_rows(fmt, d, ps, rows, room, size):
@@ -328,3 +328,41 @@ def test_later_tokens_do_not_reach_earlier_rows(fmt, d, ps, rows, room, size):
         at = slice(i * rows, (i + 1) * rows)
         _near(p, i, q[at], out[at], lse[at], first)
     assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,ps", [(64, 16), (64, 64), (128, 16)])
+@pytest.mark.parametrize("rows", [30, 100])
+def test_keys_far_apart_within_a_block(fmt, d, ps, rows):
+    """Pages of keys 2^30 times the others whose scores lie far below them: the
+    scores of the others keep their own precision."""
+    p = Pair(fmt, kvh=1, d=d, ps=ps, num_pages=90, max_pages=8192 // ps)
+
+    def large(x):  # (keys and values of one head, in that order)
+        x[:, :d] = -np.abs(x[:, :d]) * 2.0 ** 30
+
+    p.append([0], [2 * ps + 5])
+    p.append([0], [ps - 5])
+    p.append([0], [ps], mutate=large)
+    p.append([0], [3 * ps + rows])
+    q = (torch.randn(rows, 1, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").abs() + 0.1).bfloat16()
+    out, lse = torch.zeros_like(q), torch.zeros(rows, 1, device="cuda")
+    work = torch.empty(p.dev.attention_workspace_bytes(1, 1, rows, rows), dtype=torch.uint8, device="cuda")
+    p.dev.attention(0, q, out, _i32([0]), _i32([0, rows]), rows, work, lse=lse)
+    p.G.check_device_error()
+    # against the same sequence without the page: its weights are below e^-(2^20)
+    k, v = p.ref.values(0, 0)
+    keep = np.arange(len(k)) // ps != 3
+    z = np.einsum("rd,td->rt", q[:, 0].double().cpu().numpy(), k[:, 0]) / np.sqrt(d)
+    mag = np.einsum("rd,td->rt", q[:, 0].double().cpu().numpy(), np.abs(k[:, 0])) / np.sqrt(d)
+    seen = np.arange(len(k))[None] <= np.arange(len(k) - rows, len(k))[:, None]
+    assert np.all(z[:, ~keep] < -2.0 ** 20)
+    z = np.where(seen & keep, z, -np.inf)
+    m = z.max(1, keepdims=True)
+    e = np.exp(z - m)
+    want, wl = e @ v[:, 0] / e.sum(1, keepdims=True), (m + np.log(e.sum(1, keepdims=True)))[:, 0]
+    ds = 2 * d * 2.0 ** -24 * np.where(seen & keep, mag, 0).max(1)
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * ds[:, None] + 2.0 ** -14) * (e @ np.abs(v[:, 0]) / e.sum(1, keepdims=True)) \
+        + 2.0 ** -30 * len(k) * np.abs(v).max()
+    assert np.all(np.abs(out[:, 0].double().cpu().numpy() - want) <= bound)
+    assert np.all(np.abs(lse[:, 0].double().cpu().numpy() - wl) <= ds + 2.0 ** -20 * (1 + np.abs(wl)))

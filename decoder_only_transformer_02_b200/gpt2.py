@@ -262,14 +262,14 @@ class GPT2:
         """prefill into a KV8Cache: tokens device int32 [B, T0], the prefixes of
         the slots (device int32 [B]), which are freed first; next_out: device
         int32 [B]."""
-        B, T0 = tokens.shape
+        B, T0 = cache._step("gpt2_kv8_prefill", slots, tokens, next_out, 2)
         self._check(self._lib.gpt2_kv8_prefill(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, T0, temperature,
                                                top_k, seed, _ptr(next_out)))
 
     def kv8_decode_step(self, cache, slots, tokens, next_out, temperature=1.0, top_k=1, seed=0):
         """One token per slot of a KV8Cache, each at its slot's next position:
         slots, tokens, next_out device int32 [B]."""
-        B = tokens.shape[0]
+        B, = cache._step("gpt2_kv8_decode_step", slots, tokens, next_out, 1)
         self._check(self._lib.gpt2_kv8_decode_step(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, temperature,
                                                    top_k, seed, _ptr(next_out)))
 
@@ -488,6 +488,15 @@ class KV8Cache:
         if t.dtype is not self._i32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous():
             raise GPT2Error(-1, what + ": index arrays are contiguous one-dimensional int32 tensors on the cache's device")
         return len(t)
+
+    def _step(self, what, slots, tokens, next_out, dim):
+        """Shape of a model call's tokens; slots has one entry for each row, next_out at least one."""
+        if any(t is None for t in (slots, tokens, next_out)) or tokens.dtype is not self._i32 or \
+                tokens.device != self.device or tokens.dim() != dim or not tokens.is_contiguous():
+            raise GPT2Error(-1, what + ": tokens is a contiguous int32 tensor on the cache's device")
+        if self._ints(what, slots) != tokens.shape[0] or self._ints(what, next_out) < tokens.shape[0]:
+            raise GPT2Error(-1, what + ": slots and next_out have one entry for each row of tokens")
+        return tokens.shape
 
     def _work(self, what, t):
         if t.device != self.device or not t.is_contiguous():

@@ -1,0 +1,60 @@
+"""The Python side of the paged 8-bit cache without a GPU: what it refuses and
+what it hands on, with CPU tensors and a library that records its calls."""
+import contextlib
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Lib:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def made():
+    """(module, cache, model, library) around CPU tensors."""
+    from decoder_only_transformer_02_b200 import gpt2 as G
+    c, m, lib = G.KV8Cache.__new__(G.KV8Cache), G.GPT2.__new__(G.GPT2), Lib()
+    c._torch, c._i32, c._f32, c._bf16 = torch, torch.int32, torch.float32, torch.bfloat16
+    c._only_device, c.device, c._lib, c._p = True, torch.device("cpu"), lib, 1
+    c.n_kv_head, c.head_dim, c.num_slots = 2, 64, 8
+    m._h, m._lib, m.cfg = None, lib, types.SimpleNamespace(padded_vocab=512)
+    m._check = lambda r: None
+    yield G, c, m, lib
+    m._h = None
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def test_model_calls_check_their_arrays(made):
+    G, c, m, lib = made
+    good = dict(slots=i32(3), tokens=i32(3), next_out=i32(3))
+    m.kv8_decode_step(c, **good)
+    m.kv8_decode_step(c, **dict(good, next_out=i32(5)))
+    m.kv8_prefill(c, **dict(good, tokens=i32(3, 7)))
+    assert [n for n, _ in lib.calls] == ["gpt2_kv8_decode_step"] * 2 + ["gpt2_kv8_prefill"]
+    assert lib.calls[2][1][4:6] == (3, 7)
+    bad = [dict(slots=i32(2)), dict(slots=i32(4)), dict(slots=None), dict(slots=i32(3).long()), dict(slots=i32(6)[::2]),
+           dict(slots=i32(3, 1)), dict(slots=torch.zeros(3, dtype=torch.int32, device="meta")), dict(next_out=i32(2)),
+           dict(next_out=None), dict(next_out=i32(3).float()), dict(next_out=i32(6)[::2]),
+           dict(next_out=torch.zeros(3, dtype=torch.int32, device="meta"))]
+    steps = bad + [dict(tokens=i32(3).long()), dict(tokens=i32(6)[::2]), dict(tokens=i32(3, 1)), dict(tokens=None),
+                   dict(tokens=torch.zeros(3, dtype=torch.int32, device="meta"))]
+    prefills = bad + [dict(tokens=i32(3, 7).long()), dict(tokens=i32(7, 3).t()), dict(tokens=i32(3)), dict(tokens=None)]
+    for call, base, cases in ((m.kv8_decode_step, good, steps), (m.kv8_prefill, dict(good, tokens=i32(3, 7)), prefills)):
+        for i, b in enumerate(cases):
+            with pytest.raises(G.GPT2Error) as e:
+                call(c, **dict(base, **b))
+            assert e.value.name == "EINVAL", (call, i)
+    assert len(lib.calls) == 3

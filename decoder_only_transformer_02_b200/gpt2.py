@@ -509,7 +509,7 @@ class KV8Cache:
             n, h, d = t.shape
             s0, s1, s2 = t.stride()
             if h == heads and d == self.head_dim and s2 == 1 and (s1 == d or h == 1):
-                return n, (s0 if n > 1 else max(s0, h * d))
+                return n, (s0 if n > 1 else h * d)  # (the stride of a single row means nothing)
         raise GPT2Error(-1, what + ": rows are bf16 [rows, heads, head_dim] with contiguous heads on the cache's device")
 
     def resize(self, slots, new_lens, work, stream=None):

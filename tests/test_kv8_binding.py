@@ -58,3 +58,20 @@ def test_model_calls_check_their_arrays(made):
                 call(c, **dict(base, **b))
             assert e.value.name == "EINVAL", (call, i)
     assert len(lib.calls) == 3
+
+
+def test_a_single_row_may_have_any_stride(made):
+    """torch leaves the stride of a dimension of one entry open: keys and values
+    of one token out of different buffers are of the same shape all the same."""
+    G, c, m, lib = made
+    bf = dict(dtype=torch.bfloat16)
+    k = torch.zeros(1, 5, 64, **bf)[:, :2]                             # row stride 320
+    v = torch.as_strided(torch.zeros(128, **bf), (1, 2, 64), (1, 64, 1))  # row stride 1
+    cu = torch.tensor([0, 1], dtype=torch.int32)
+    c.append(0, k, v, i32(1), cu)
+    c.append(0, k[:0], v[:0], i32(1), cu)
+    q = torch.as_strided(torch.zeros(259, **bf), (1, 4, 64), (257, 64, 1))
+    c.attention(0, q, q, i32(1), cu, 1, torch.zeros(64, dtype=torch.uint8))
+    assert [a[1][4] for a in lib.calls[:2]] == [128, 128] and lib.calls[2][1][3] == lib.calls[2][1][5] == 256
+    with pytest.raises(G.GPT2Error):
+        c.append(0, torch.zeros(2, 5, 64, **bf)[:, :2], torch.zeros(2, 2, 64, **bf), i32(1), cu)

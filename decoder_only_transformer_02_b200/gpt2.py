@@ -472,14 +472,17 @@ class KV8Cache:
         return int(self._lib.gpt2_kv8_workspace_bytes(self._p, n))
 
     def attention_workspace_bytes(self, n_head, n, rows, max_q) -> int:
-        return int(self._lib.gpt2_kv8_attention_workspace_bytes(self._p, n_head, n, rows, max_q))
+        # (it goes by the number of SMs of the current device)
+        return int(self._on_device(self._lib.gpt2_kv8_attention_workspace_bytes, self._p, n_head, n, rows, max_q))
+
+    def _on_device(self, fn, *args):
+        if self._only_device or self._torch.cuda.current_device() == self.device.index:
+            return fn(*args)
+        with self._torch.cuda.device(self.device):
+            return fn(*args)
 
     def _call(self, what, fn, *args):
-        if self._only_device or self._torch.cuda.current_device() == self.device.index:
-            r = fn(*args)
-        else:
-            with self._torch.cuda.device(self.device):
-                r = fn(*args)
+        r = self._on_device(fn, *args)
         if r != 0:
             raise GPT2Error(r, what)
 

@@ -1,6 +1,7 @@
 """The Python side of the paged 8-bit cache without a GPU: what it refuses and
 what it hands on, with CPU tensors and a library that records its calls."""
 import contextlib
+import contextlib
 import types
 
 import pytest
@@ -75,3 +76,27 @@ def test_a_single_row_may_have_any_stride(made):
     assert [a[1][4] for a in lib.calls[:2]] == [128, 128] and lib.calls[2][1][3] == lib.calls[2][1][5] == 256
     with pytest.raises(G.GPT2Error):
         c.append(0, torch.zeros(2, 5, 64, **bf)[:, :2], torch.zeros(2, 2, 64, **bf), i32(1), cu)
+
+
+def test_calls_run_on_the_caches_device(made):
+    """Also the size of the attention's workspace, which goes by its SMs."""
+    G, c, m, lib = made
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        now[0], was = d.index, now[0]
+        yield
+        now[0] = was
+
+    class Calls:
+        def __getattr__(self, name):
+            return lambda *args: now[0] if name.endswith("bytes") else lib.calls.append((name, now[0])) or 0
+
+    c._lib, c._only_device = Calls(), False
+    c._torch = types.SimpleNamespace(cuda=types.SimpleNamespace(current_device=lambda: now[0], device=device))
+    dev, c.device = c.device, torch.device("cuda", 3)
+    assert c.attention_workspace_bytes(2, 1, 1, 1) == 3 and now == [0]
+    c._call("x", c._lib.gpt2_kv8_fork)
+    assert lib.calls == [("gpt2_kv8_fork", 3)] and now == [0]
+    c.device = dev

@@ -246,17 +246,21 @@ class GPT2:
         self._check(self._lib.gpt2_set_graphs(self._h, 1 if enable else 0))
 
     # -- generation
+    _dec_rows = 0  # rows of the last call's logits
+
     def prefill(self, tokens, next_out, temperature=1.0, top_k=1, seed=0):
         """tokens: device int32 [B, T0]; next_out: device int32 [B] (receives
         the token at position T0)."""
         B, T0 = tokens.shape
         self._check(self._lib.gpt2_prefill(self._h, _ptr(tokens), B, T0, temperature, top_k, seed, _ptr(next_out)))
+        self._dec_rows = B
 
     def decode_step(self, tokens, pos, next_out, temperature=1.0, top_k=1, seed=0):
         """tokens: device int32 [B] at position pos; next_out: device int32 [B]."""
         B = tokens.shape[0]
         self._check(self._lib.gpt2_decode_step(self._h, _ptr(tokens), B, pos, temperature, top_k, seed,
                                                _ptr(next_out)))
+        self._dec_rows = B
 
     def kv8_prefill(self, cache, slots, tokens, next_out, temperature=1.0, top_k=1, seed=0):
         """prefill into a KV8Cache: tokens device int32 [B, T0], the prefixes of
@@ -265,6 +269,7 @@ class GPT2:
         B, T0 = cache._step("gpt2_kv8_prefill", slots, tokens, next_out, 2)
         self._check(self._lib.gpt2_kv8_prefill(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, T0, temperature,
                                                top_k, seed, _ptr(next_out)))
+        self._dec_rows = B
 
     def kv8_decode_step(self, cache, slots, tokens, next_out, temperature=1.0, top_k=1, seed=0):
         """One token per slot of a KV8Cache, each at its slot's next position:
@@ -272,11 +277,17 @@ class GPT2:
         B, = cache._step("gpt2_kv8_decode_step", slots, tokens, next_out, 1)
         self._check(self._lib.gpt2_kv8_decode_step(self._h, cache.handle, _ptr(slots), _ptr(tokens), B, temperature,
                                                    top_k, seed, _ptr(next_out)))
+        self._dec_rows = B
 
     def get_decode_logits(self, B) -> np.ndarray:
-        a = np.empty((B, self.cfg.padded_vocab), dtype=np.float32)
+        """The first B rows of the logits of the last prefill or decode step,
+        dense or paged."""
+        rows = self._dec_rows  # (the library writes all of them)
+        a = np.empty((max(B, rows), self.cfg.padded_vocab), dtype=np.float32)
         self._check(self._lib.gpt2_get_decode_logits(self._h, a.ctypes.data))
-        return a
+        if B > rows:
+            raise GPT2Error(-1, f"the last call had {rows} rows")
+        return a[:B]
 
     # -- measurement support
     def set_timing(self, enable: bool):

@@ -100,3 +100,33 @@ def test_calls_run_on_the_caches_device(made):
     c._call("x", c._lib.gpt2_kv8_fork)
     assert lib.calls == [("gpt2_kv8_fork", 3)] and now == [0]
     c.device = dev
+
+
+def test_decode_logits_have_room_for_the_last_calls_rows(made, monkeypatch):
+    """A paged step of four rows between two dense ones of two: the library
+    writes four rows whatever the caller asks for."""
+    import numpy as np
+    G, c, m, lib = made
+    heap, room = np.full((16, 512), np.nan, np.float32), []
+
+    class Np:
+        def __getattr__(self, name):
+            return getattr(np, name)
+
+        def empty(self, shape, dtype):
+            room.append(shape[0])
+            return heap[:shape[0]]
+
+    class Writes(Lib):
+        def gpt2_get_decode_logits(self, h, p):
+            heap[:4] = np.arange(4)[:, None]
+            return 0
+
+    m._lib = Writes()
+    monkeypatch.setattr(G, "np", Np())
+    m.kv8_decode_step(c, i32(4), i32(4), i32(4))
+    got = m.get_decode_logits(2)
+    assert room == [4] and got.shape == (2, 512) and np.all(got == [[0], [1]])
+    assert m.get_decode_logits(4).shape == (4, 512)
+    with pytest.raises(G.GPT2Error):
+        m.get_decode_logits(5)

@@ -142,10 +142,10 @@ constexpr int APPEND_WARPS = 8;
 // its q tokens touch at most q / ps + 2 pages; no prefix sum is needed.
 // HELD: 16-byte pieces of a tile that a lane keeps between the two passes: 1 for
 // short runs, 4 (a tile of 1024 values) for prompts; the rest is read again, UN
-// pieces at a time: 1 where nothing is left (17.7 us; with 4, whose registers
+// pieces at a time: 1 where nothing is left (17.9 us; with 4, whose registers
 // cost warps, 20.0), 4 where tiles are larger (64 tokens of 64: 22.5; with 1, 30).
 // What it moves: 2 bytes in, 1 out per value.  15,400 rows of 2 x 768 values:
-// 17.8 us (3.9 TB/s; 25.7 with both passes reading, 22 with 8 pieces held, whose
+// 17.9 us (3.9 TB/s; 25.7 with both passes reading, 22 with 8 pieces held, whose
 // registers cost half the warps); 256 single rows: 5.8 us, its chain of loads.
 template <int FMT, int HELD, int UN>
 __global__ void __launch_bounds__(32 * APPEND_WARPS)

@@ -13,8 +13,9 @@
 //  - S^T = K Q^T and O^T = V^T P^T on mma m16n8k16 (f16 in, fp32 out), tokens
 //    (then dimensions) in the 16 rows and 8 query rows in the columns: with few
 //    rows this wastes half as much of an instruction as rows in the 16 would.
-//    (tcgen05's smallest tile has 64 rows and takes its operands from shared
-//    memory, 16 times the work of these products at one query row.)
+//    (tcgen05 could have tokens in its 64 or more rows and 8 query rows in the
+//    columns too, but takes the tokens' operand from shared memory: the converted
+//    codes would be stored there and read once more.)
 //  - A thread's 16 bytes of a key are its A operand: which dimension stands at
 //    which k index is free as long as Q agrees, so no code moves between lanes.
 //    The values' operand pairs two tokens of one dimension, a byte permute.
@@ -29,7 +30,7 @@
 //  - Each warp keeps three 4 KB steps of codes in flight (asynchronous copies
 //    into a ring of its own).  Loading the next step into registers instead
 //    kept a third as many bytes in flight: 131 us where this took 118 (32
-//    sequences of up to 16384 tokens, 705 MB: 6.0 TB/s of 6.56 measured).
+//    sequences of up to 16384 tokens, 705 MB; 116.5 by now, 6.1 TB/s of 6.56 measured).
 //  - All sequences' 16-token groups, tile after tile (a tile: the rows of one
 //    sequence and key/value head), are one line of work that is cut into equal
 //    parts, one per CTA; a part's warps take its steps in turn.  A tile
@@ -761,9 +762,10 @@ static inline int sm_count() {
 }
 
 // Sequences with more rows per key/value head than this go to the tensor-core
-// kernel of kv8_prompt.cuh.  16 sequences of 4096: 64 rows take 96.6 us here, 65
-// take 94.5 there; 64 sequences of 1024: 102 and 133; d = 128: 169 and 168.  Below,
-// the streaming kernel wins (32 rows: 62, 57 and 101 us).
+// kernel of kv8_prompt.cuh.  64 rows here and 65 there, d = 64: 16 sequences of
+// 4096 93 and 107 us, 64 of 1024 110 and 150; d = 128: 181 and 168, 209 and 213.
+// Twice as many rows cost here twice as much (32 rows: 55 and 61 us; 102 and 114),
+// there next to nothing (96 rows: 108 and 152; 172 and 219).
 constexpr int NARROW_ROWS = 64;
 static inline long narrow_rows(long rows) { return rows < NARROW_ROWS ? rows : NARROW_ROWS; }
 
@@ -814,8 +816,13 @@ static inline cudaError_t stream_launch(const Call& k, void* work, cudaStream_t 
   return launch_after(join_kernel<D, S::RT>, dim3(grid, join_ctas(S::RT)), 32 * J_WARPS, 0, st, a);
 }
 // Where no slot can hold more than this, every tile is one CTA's: no line, no
-// join.  64 sequences of 1 to 1024 tokens: 19.8 us, and cut into parts 23.8;
-// one sequence of 777: 6.3 (eight warps; sixteen 7.2), and cut 8.9.
+// join.  Sequences of 1024, whole and cut into parts: one 6.8 and 8.0 us, 8 7.4 and
+// 10.1, 64 25.2 and 29.4; of 2032: 10.2 and 8.5, 11.4 and 13.1, 42.6 and 46.4; of
+// 4080: 16.7 and 9.6, 18.9 and 19.5, 76.9 and 77.9.  d = 128, 8 heads, 1024: 10.5
+// and 9.5, 10.6 and 11.9, 32.9 and 34.3; 2032: 16.2 and 10.3, 17.9 and 16.1, 57.7 and
+// 52.9.  (One sequence alone would want the parts from 1300 tokens on, at d = 128
+// from 900; it goes by the table's width, since the lengths are on the device.)
+// One sequence of 777: 6.4 with eight warps, sixteen 7.2.
 constexpr long WHOLE_TOKENS = 2048;
 static inline bool whole_tiles(const Cache& c) { return (long)c.max_pages * c.ps <= WHOLE_TOKENS; }
 template <int FMT, int D, int NT, bool MANY>

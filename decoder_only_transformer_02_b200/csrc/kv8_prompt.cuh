@@ -33,11 +33,12 @@
 // kernel: four chunks of 300 to 1024 rows are 120 items of unequal length, which
 // taken whole would leave SMs idle and others twice as busy.
 //
-// Measured: 64 sequences of 256 new tokens over 4096, 12 heads: 419 us at d = 64
-// (476 TFLOP/s), 677 at d = 128 (590); one tile per item (128 new tokens) 327 us;
-// four chunks of 300 to 1024 over 1500 to 4096: 62 us.  The exponentials bound it
-// (MUFU 16 a cycle: 1.1 us of the 2.6 of a block with two tiles) together with the
-// softmax warps' latency, and at d = 128 the conversion.
+// Measured: 64 sequences of 256 new tokens over 4096, 12 heads: 447 us at d = 64
+// (447 TFLOP/s), 696 at d = 128 (574; e4m3 682); one tile per item (128 new tokens)
+// 372 us; four chunks of 300 to 1024 over 1500 to 4096: 62 us.  The softmax warps'
+// chain from TMEM load to store bounds it (MUFU 45% busy, tensor pipe 22%), and at
+// d = 128 the conversion.  With 128 registers a thread, 22 words are spilled and
+// 53 (63) read back.
 //
 // All waits are bounded.
 #pragma once

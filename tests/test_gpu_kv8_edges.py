@@ -366,3 +366,37 @@ def test_keys_far_apart_within_a_block(fmt, d, ps, rows):
         + 2.0 ** -30 * len(k) * np.abs(v).max()
     assert np.all(np.abs(out[:, 0].double().cpu().numpy() - want) <= bound)
     assert np.all(np.abs(lse[:, 0].double().cpu().numpy() - wl) <= ds + 2.0 ** -20 * (1 + np.abs(wl)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [30, 100])
+@pytest.mark.parametrize("side", [0, 1])
+def test_far_apart_and_not_a_number_in_one_block(fmt, d, rows, side):
+    """Ordinary, large and NaN pages, and one outside the pool, within 128 tokens."""
+    p = Pair(fmt, kvh=1, d=d, ps=16, num_pages=90, max_pages=512)
+    p.append([0], [208])
+    p.append([0], [16], size=2.0 ** 35)
+    p.append([0], [16])
+
+    def bad(x):  # (keys, then values)
+        x[3, side * d + 5] = np.inf
+
+    p.append([0], [16], mutate=bad)
+    p.append([0], [16], size=2.0 ** -30)
+    q = torch.randn(rows, 2, d, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    work = torch.empty(p.dev.attention_workspace_bytes(2, 1, rows, rows), dtype=torch.uint8, device="cuda")
+    for first in (240, 224):  # the NaN page; then a page before it outside the pool too
+        out, lse = torch.zeros_like(q), torch.zeros(rows, 2, device="cuda")
+        p.dev.attention(0, q[-rows:], out, _i32([0]), _i32([0, rows]), rows, work, lse=lse)
+        if first == 240:
+            p.G.check_device_error()
+        else:
+            with pytest.raises(p.G.GPT2Error):
+                p.G.check_device_error()
+        n = 272
+        sees = torch.arange(n - rows, n, device="cuda") >= first
+        if (~sees).any():
+            _near(p, 0, q, out, lse, first)
+        assert torch.isnan(out[sees].float()).all()
+        p.dev.table[0, 14] = -1

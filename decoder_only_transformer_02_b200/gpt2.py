@@ -505,6 +505,8 @@ class KV8Cache:
 
     def _step(self, what, slots, tokens, next_out, dim):
         """Shape of a model call's tokens; slots has one entry for each row, next_out at least one."""
+        if not self._only_device and self._torch.cuda.current_device() != self.device.index:
+            raise GPT2Error(-1, what + ": a model's calls run on the current device, the cache is on another one")
         if any(t is None for t in (slots, tokens, next_out)) or tokens.dtype is not self._i32 or \
                 tokens.device != self.device or tokens.dim() != dim or not tokens.is_contiguous():
             raise GPT2Error(-1, what + ": tokens is a contiguous int32 tensor on the cache's device")

@@ -130,3 +130,15 @@ def test_decode_logits_have_room_for_the_last_calls_rows(made, monkeypatch):
     assert m.get_decode_logits(4).shape == (4, 512)
     with pytest.raises(G.GPT2Error):
         m.get_decode_logits(5)
+
+
+def test_model_calls_refuse_a_cache_on_another_device(made):
+    G, c, m, lib = made
+    now = [0]
+    c._only_device, c.device = False, torch.device("cuda", 3)
+    c._torch = types.SimpleNamespace(cuda=types.SimpleNamespace(current_device=lambda: now[0]))
+    for call, tokens in ((m.kv8_decode_step, i32(2)), (m.kv8_prefill, i32(2, 3))):
+        with pytest.raises(G.GPT2Error, match="current device") as e:
+            call(c, i32(2), tokens, i32(2))
+        assert e.value.name == "EINVAL"
+    assert lib.calls == []

@@ -33,9 +33,9 @@
 // kernel: four chunks of 300 to 1024 rows are 120 items of unequal length, which
 // taken whole would leave SMs idle and others twice as busy.
 //
-// Measured: 64 sequences of 256 new tokens over 4096, 12 heads: 447 us at d = 64
-// (447 TFLOP/s), 696 at d = 128 (574; e4m3 682); one tile per item (128 new tokens)
-// 372 us; four chunks of 300 to 1024 over 1500 to 4096: 62 us.  The softmax warps'
+// Measured: 64 sequences of 256 new tokens over 4096, 12 heads: 443 us at d = 64
+// (451 TFLOP/s), 683 at d = 128 (585); one tile per item (128 new tokens) 356 us;
+// four chunks of 300 to 1024 over 1500 to 4096: 62 us.  The softmax warps'
 // chain from TMEM load to store bounds it (MUFU 45% busy, tensor pipe 22%), and at
 // d = 128 the conversion.  With 128 registers a thread, 22 words are spilled and
 // 53 (63) read back.
@@ -215,9 +215,9 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // scores may pass 2^20 (a sum of products is below 2^30): there the fused z of the
 // common case would differ from the maximum, which is rounded, by half their last
 // place.  Rare, so the loop over the blocks is left for it and entered again: as a
-// branch in the loop it made the common case slower by a tenth (of which a twentieth
-// is left: 64 sequences of 256 over 4096 427 -> 447 us, at d = 128 679 -> 682; one
-// tile per item 346 -> 373; four chunks 61.6 -> 62.4).
+// branch in the loop it made the common case slower by a tenth (of which 3% are
+// left: 64 sequences of 256 over 4096 427 -> 442 us, one tile per item 346 -> 356,
+// four chunks 61.7 -> 62.4; nothing at d = 128).
 template <int D>
 __device__ __noinline__ void far_rescale(uint32_t tl, float f) {  // the row's O
   tcg::tc_fence_after();
@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) wide_kernel(const Call k) {
           const float vmax = __uint_as_float(max(1u << 23, __reduce_max_sync(0xffffffffu, nan ? 0u : __float_as_uint(fabsf(vs)))));
           vref = fmaxf(vref, vmax);
           kexp = __float_as_uint(kmax) >> 23, vexp = __float_as_uint(vmax) >> 23;
-          const float kr = apart ? 1.f : ks * (1.f / kmax), vr = apart ? 1.f : vs * (1.f / vref);
+          // (the conversion waits for this: divisions in place of the powers' inverses make 442 us 447, one tile 356 372)
+          const float kr = apart ? 1.f : ks * inverse_pow2(__float_as_uint(kmax)), vr = apart ? 1.f : vs * inverse_pow2(__float_as_uint(vref));
           // a page with a scale that is not a number: its keys are not, its values 0 (only rows that see it notice)
           const uint32_t kf = nan ? 0x7e007e00u : half2_of(kr, kr), vf = nan ? 0u : half2_of(vr, vr);
           if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[s], ((g / NS) & 1u) ^ 1u))) {

@@ -763,9 +763,9 @@ static inline int sm_count() {
 
 // Sequences with more rows per key/value head than this go to the tensor-core
 // kernel of kv8_prompt.cuh.  64 rows here and 65 there, d = 64: 16 sequences of
-// 4096 93 and 107 us, 64 of 1024 110 and 150; d = 128: 181 and 168, 209 and 213.
+// 4096 93 and 103 us, 64 of 1024 110 and 146; d = 128: 181 and 166, 209 and 211.
 // Twice as many rows cost here twice as much (32 rows: 55 and 61 us; 102 and 114),
-// there next to nothing (96 rows: 108 and 152; 172 and 219).
+// there next to nothing (96 rows: 104 and 148; 170 and 216).
 constexpr int NARROW_ROWS = 64;
 static inline long narrow_rows(long rows) { return rows < NARROW_ROWS ? rows : NARROW_ROWS; }
 

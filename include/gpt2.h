@@ -330,7 +330,8 @@ size_t gpt2_kv8_attention_workspace_bytes(const gpt2_kv8* cache, int n_head, int
  * ldq / ldo elements apart (multiples of 8, pointers 16-byte aligned); query
  * head j reads key/value head j / (n_head / n_kv_head); n_head is a multiple
  * of n_kv_head, at most 64 times it.  d_slots, d_cu, n, rows as for
- * gpt2_kv8_append: row r of slot s sees that slot's tokens up to its own.
+ * gpt2_kv8_append: row r of slot s sees that slot's tokens up to its own, and
+ * nothing of later ones, whatever their size.
  * max_q: no sequence has more rows than this (host value; larger ones are
  * skipped and recorded).  d_lse (may be NULL): fp32 [rows][n_head], natural
  * log of the softmax denominators.  Rows that belong to no sequence, and those

@@ -400,3 +400,25 @@ def test_far_apart_and_not_a_number_in_one_block(fmt, d, rows, side):
             _near(p, 0, q, out, lse, first)
         assert torch.isnan(out[sees].float()).all()
         p.dev.table[0, 14] = -1
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [30, 100])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3.0e38])
+def test_a_query_that_is_not_finite_stays_in_its_row(d, rows, value):
+    p = Pair(R.E4M3, kvh=1, d=d, ps=16, num_pages=90, max_pages=512)
+    p.append([0], [400])
+    q = torch.randn(rows, 1, d, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").bfloat16()
+    work = torch.empty(p.dev.attention_workspace_bytes(1, 1, rows, rows), dtype=torch.uint8, device="cuda")
+    want, wl, mag, top = p.ref.attention(0, q.double().cpu().numpy(), [0], [0, rows])
+    q[rows // 2, 0, 7] = value
+    out, lse = torch.zeros_like(q), torch.zeros(rows, 1, device="cuda")
+    p.dev.attention(0, q, out, _i32([0]), _i32([0, rows]), rows, work, lse=lse)
+    p.G.check_device_error()
+    k = np.arange(rows) != rows // 2
+    ds = 2 * d * 2.0 ** -24 * top[k]
+    v = np.abs(p.ref.values(0, 0)[1]).max()
+    bound = 2.0 ** -8 * np.abs(want[k]) + (2.0 ** -11 + 2 * ds[..., None] + 2.0 ** -14) * mag[k] + 2.0 ** -30 * 400 * v
+    assert np.all(np.abs(out.double().cpu().numpy()[k] - want[k]) <= bound)
+    assert np.all(np.abs(lse.double().cpu().numpy()[k] - wl[k]) <= ds + 2.0 ** -20 * (1 + np.abs(wl[k])))
+    assert value == 3.0e38 or not torch.isfinite(lse[rows // 2]).any()

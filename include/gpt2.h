@@ -355,7 +355,8 @@ int gpt2_kv8_attention(const gpt2_kv8* cache, int layer, const void* d_q, int64_
  * nothing enqueued); what was allocated stays until gpt2_destroy, so graphs
  * captured earlier can still be replayed.  A call that the cache refuses
  * (GPT2_ECACHE at the next syncing call) leaves the cache as it was, except
- * that a refused prefill has freed its slots; d_next is then meaningless.
+ * that a prefill refused for want of pages has freed its slots; d_next is then
+ * meaningless.
  * Prefill: the slots are freed and hold positions 0 .. T0-1 of d_tokens
  * [B, T0] (T0 <= max_T) afterwards; the prefix itself attends to its unrounded
  * keys and values. */
